@@ -20,8 +20,14 @@ from .binding import (FLAG_BAD_EXPERT, FLAG_BAD_SCALE, FLAG_BOUNDS, FLAG_LAYOUT,
                       MOE_OPT_WAIT_LIMIT_US, MOE_OPT_TEST_TIMEOUT, MOE_OPT_TC_A_TMEM,
                       MOE_OPT_TC_FORM,
                       moe_sort_static, moe_layer_forward_with_router, moe_layer_router_workspace_bytes,
-                      moe_fp8_pack_weights, moe_fp8_unpack_weights, moe_fp8_linear)
+                      moe_fp8_pack_weights, moe_fp8_unpack_weights, moe_fp8_linear,
+                      moe_balance_workspace_bytes, moe_balance_loss, moe_route_backward,
+                      moe_router_backward_workspace_bytes, moe_router_logits_backward,
+                      moe_ckpt_pack, moe_ckpt_unpack, moe_ckpt_swiglu_backward,
+                      moe_ckpt_wgrad_workspace_bytes, moe_ckpt_wgrad)
 
 __all__ = ["moe_layer_forward", "moe_layer_tables", "moe_layer_workspace_bytes", "make_debug", "moe_pack_weights", "moe_unpack_weights", "moe_router_logits", "moe_route", "moe_sort", "moe_forward",
            "moe_quant_rows_f32", "moe_exp_f32", "moe_swiglu_f32", "moe_check_device_flag", "moe_packed_bytes", "moe_workspace_bytes",
-           "moe_sort_workspace_bytes", "MoeError", "LIB_PATH", "SYMBOLS", "lib"]
+           "moe_sort_workspace_bytes", "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward",
+           "moe_router_backward_workspace_bytes", "moe_router_logits_backward", "moe_ckpt_pack", "moe_ckpt_unpack",
+           "moe_ckpt_swiglu_backward", "moe_ckpt_wgrad_workspace_bytes", "moe_ckpt_wgrad", "MoeError", "LIB_PATH", "SYMBOLS", "lib"]

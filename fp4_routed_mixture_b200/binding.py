@@ -8,6 +8,7 @@ importing this module without the built library raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -29,6 +30,10 @@ SYMBOLS = ["moe_last_error", "moe_packed_bytes", "moe_pack_weights", "moe_unpack
            "moe_quant_rows_f32", "moe_exp_f32", "moe_swiglu_f32",
            "moe_fp8_packed_bytes", "moe_fp8_pack_weights", "moe_fp8_unpack_weights", "moe_fp8_workspace_bytes",
            "moe_fp8_linear",
+           "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward",
+           "moe_router_backward_workspace_bytes", "moe_router_logits_backward",
+           "moe_ckpt_pack", "moe_ckpt_unpack", "moe_ckpt_swiglu_backward",
+           "moe_ckpt_wgrad_workspace_bytes", "moe_ckpt_wgrad",
            "moe_set_option", "moe_get_option", "moe_launch_count", "moe_check_device_flag"]
 
 
@@ -79,6 +84,16 @@ def _load():
         "moe_fp8_unpack_weights": ([i32, i32, vp, vp, vp, vp], i32),
         "moe_fp8_workspace_bytes": ([i32, i32, i32], sz),
         "moe_fp8_linear": ([vp, i32, i32, i32, vp, vp, vp, sz, vp, vp, vp], i32),
+        "moe_balance_workspace_bytes": ([i32, i32, i32], sz),
+        "moe_balance_loss": ([vp, vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, sz, vp], i32),
+        "moe_route_backward": ([vp] * 9 + [i32, i32, i32, i32, ctypes.c_float, vp, vp, vp], i32),
+        "moe_router_backward_workspace_bytes": ([i32, i32, i32], sz),
+        "moe_router_logits_backward": ([vp] * 5 + [i32, i32, i32, vp, vp, vp, i32, vp, sz, vp], i32),
+        "moe_ckpt_pack": ([vp, ctypes.c_int64, i32, i32, vp, vp, vp], i32),
+        "moe_ckpt_unpack": ([vp, vp, i32, i32, vp, ctypes.c_int64, vp], i32),
+        "moe_ckpt_swiglu_backward": ([vp, vp, vp, ctypes.c_int64, i32, i32, vp, vp, vp], i32),
+        "moe_ckpt_wgrad_workspace_bytes": ([i32, i32, i32, i32], sz),
+        "moe_ckpt_wgrad": ([vp, ctypes.c_int64] + [vp] * 4 + [i32] * 6 + [vp, i32, vp, sz, vp], i32),
         "moe_set_option": ([i32, i32], i32),
         "moe_get_option": ([i32], i32),
         "moe_launch_count": ([], ctypes.c_ulonglong),
@@ -380,6 +395,258 @@ def moe_fp8_linear(x, packed, N: int, ws=None, y=None, debug: dict | None = None
     _check(lib.moe_fp8_linear(_ptr(x), T, N, K, _ptr(packed), _ptr(y), _ptr(ws), ws.numel(), _ptr(dq), _ptr(ds),
                               _stream(stream)))
     return y
+
+
+# ---- training: balance loss, gradients, 8-bit checkpoints -----------------------------
+#
+# These calls check each tensor (device, type, shape, strides) and raise
+# MoeError(MOE_ERR_INVALID_ARG) with its name.  They run on the device of their
+# tensors, whichever device is current, on that device's current stream or on
+# `stream`.
+
+def _bad(msg: str):
+    raise MoeError(-1, msg)
+
+
+def _arg(t, name: str, dtype, shape, dev, strided: bool = False):
+    """Pointer of a checked tensor (None passes as NULL).  strided: a 2-D tensor
+    whose rows may lie further apart than their length."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _bad(f"{name} must be a CUDA tensor")
+    if t.device != dev:
+        _bad(f"{name} is on {t.device}, the call runs on {dev}")
+    if t.dtype != dtype:
+        _bad(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        _bad(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if not t.is_contiguous() and not (strided and t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
+        _bad(f"{name} must be contiguous" + (" in its rows" if strided else ""))
+    return t.data_ptr()
+
+
+def _row_stride(t) -> int:
+    """Elements between the rows of a checked 2-D tensor (a single row's stride
+    means nothing and counts as its length)."""
+    return t.stride(0) if t.shape[0] > 1 and not t.is_contiguous() else t.shape[1]
+
+
+def _matrix(t, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        _bad(f"{name} must be a 2-D CUDA tensor")
+    return t.shape
+
+
+def _mask_arg(t, T, dev):
+    if t is not None and isinstance(t, torch.Tensor) and t.dtype == torch.bool:
+        t = t.view(torch.uint8)
+    return _arg(t, "token_mask", torch.uint8, (T,), dev)
+
+
+def _ws_arg(ws, nbytes: int, dev):
+    """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
+    if nbytes == 0:
+        raise MoeError(-2, "unsupported dims")
+    if ws is None:
+        ws = _empty_aligned(nbytes, dev)
+    return ws, _arg(ws, "ws", torch.uint8, (ws.numel(),), dev), ws.numel()
+
+
+def _allocates(fn):
+    """With a `stream`, what the call allocates belongs to that stream (memory
+    of the current one may still be in use there)."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kw)
+    return call
+
+
+def _call(dev, fn, args, stream):
+    """fn(*args, stream) with the tensors' device current."""
+    if stream is not None and stream.device != dev:
+        _bad(f"stream is on {stream.device}, the tensors on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def moe_balance_workspace_bytes(T_max: int, E: int, S_max: int = 1) -> int:
+    n = lib.moe_balance_workspace_bytes(T_max, E, S_max)
+    if n == 0:
+        raise MoeError(-2, "unsupported dims")
+    return n
+
+
+@_allocates
+def moe_balance_loss(logits, topk_idx, coef: float, seq_offsets=None, token_mask=None, ws=None, out=None,
+                     stream=None):
+    """logits [T,E] fp32, topk_idx [T,k] int32, seq_offsets [S+1] int32 or None
+    (one sequence), token_mask [T] bool/uint8 or None -> (loss [1] fp32, counts
+    [S,E] int32, mean_prob [S,E] fp32, tokens [S+1] int32); `out` may hold the
+    four tensors (mean_prob None: not computed)."""
+    T, E = _matrix(logits, "logits")
+    k = _matrix(topk_idx, "topk_idx")[1]
+    dev = logits.device
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    if out is None:
+        out = (torch.empty(1, dtype=torch.float32, device=dev),
+               torch.empty((max(S, 0), E), dtype=torch.int32, device=dev),
+               torch.empty((max(S, 0), E), dtype=torch.float32, device=dev),
+               torch.empty(max(S, 0) + 1, dtype=torch.int32, device=dev))
+    loss, counts, mean_prob, tokens = out
+    p = (_arg(logits, "logits", torch.float32, (T, E), dev), _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+         _arg(seq_offsets, "seq_offsets", torch.int32, (S + 1,), dev), _mask_arg(token_mask, T, dev))
+    o = (_arg(counts, "counts", torch.int32, (S, E), dev), _arg(mean_prob, "mean_prob", torch.float32, (S, E), dev),
+         _arg(tokens, "tokens", torch.int32, (S + 1,), dev), _arg(loss, "loss", torch.float32, (1,), dev))
+    ws, pw, nw = _ws_arg(ws, lib.moe_balance_workspace_bytes(T, E, S), dev)
+    _call(dev, lib.moe_balance_loss, (*p, T, E, k, S, coef, *o, pw, nw), stream)
+    return out
+
+
+@_allocates
+def moe_route_backward(logits, topk_idx, gates=None, dgates=None, dloss=None, coef: float = 0.0, counts=None,
+                       tokens=None, seq_offsets=None, token_mask=None, ws=None, out=None, stream=None):
+    """Gradient of the logits [T,E] fp32 from the gates' gradient dgates [T,k]
+    fp32 (with moe_route's gates) and the balance loss's dloss [1] fp32 (with
+    what moe_balance_loss took and gave); either may be None.  ws: a workspace
+    (or one int32 as 4 bytes) whose error word receives MOE_FLAG_BAD_EXPERT."""
+    T, E = _matrix(logits, "logits")
+    k = _matrix(topk_idx, "topk_idx")[1]
+    dev = logits.device
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    if out is None:
+        out = torch.empty((T, E), dtype=torch.float32, device=dev)
+    if ws is not None and ws.numel() < 4:
+        _bad("ws must hold at least 4 bytes")
+    p = (_arg(logits, "logits", torch.float32, (T, E), dev), _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+         _arg(gates, "gates", torch.float32, (T, k), dev), _arg(dgates, "dgates", torch.float32, (T, k), dev),
+         _arg(dloss, "dloss", torch.float32, (1,), dev), _arg(counts, "counts", torch.int32, (S, E), dev),
+         _arg(tokens, "tokens", torch.int32, (S + 1,), dev),
+         _arg(seq_offsets, "seq_offsets", torch.int32, (S + 1,), dev), _mask_arg(token_mask, T, dev))
+    po = _arg(out, "out", torch.float32, (T, E), dev)
+    pw = None if ws is None else _arg(ws, "ws", torch.uint8, (ws.numel(),), dev)
+    _call(dev, lib.moe_route_backward, (*p, T, E, k, S, coef, po, pw), stream)
+    return out
+
+
+def moe_router_backward_workspace_bytes(T_max: int, H: int, E: int) -> int:
+    n = lib.moe_router_backward_workspace_bytes(T_max, H, E)
+    if n == 0:
+        raise MoeError(-2, "unsupported dims")
+    return n
+
+
+@_allocates
+def moe_router_logits_backward(dlogits, w_router, x=None, codes=None, scales=None, accumulate: bool = False, ws=None,
+                               out=None, stream=None):
+    """dlogits [T,E] fp32, w_router [E,H] fp32, and x [T,H] bf16 or its 8-bit
+    checkpoint (codes, scales) -> (dx [T,H] bf16, dw [E,H] fp32, dbias [E] fp32).
+    `out` may hold the three tensors, None for one not wanted; accumulate adds
+    to the dw and dbias of `out`."""
+    T, E = _matrix(dlogits, "dlogits")
+    H = _matrix(w_router, "w_router")[1]
+    dev = dlogits.device
+    if out is None:
+        if accumulate:
+            _bad("accumulate needs out")
+        out = (torch.empty((T, H), dtype=torch.bfloat16, device=dev),
+               torch.empty((E, H), dtype=torch.float32, device=dev),
+               torch.empty(E, dtype=torch.float32, device=dev))
+    dx, dw, db = out
+    p = (_arg(dlogits, "dlogits", torch.float32, (T, E), dev), _arg(x, "x", torch.bfloat16, (T, H), dev),
+         _arg(codes, "codes", torch.uint8, (T, H), dev), _arg(scales, "scales", torch.uint8, (T, H // 128), dev),
+         _arg(w_router, "w_router", torch.float32, (E, H), dev))
+    o = (_arg(dx, "dx", torch.bfloat16, (T, H), dev), _arg(dw, "dw", torch.float32, (E, H), dev),
+         _arg(db, "dbias", torch.float32, (E,), dev))
+    ws, pw, nw = _ws_arg(ws, lib.moe_router_backward_workspace_bytes(T, H, E), dev)
+    _call(dev, lib.moe_router_logits_backward, (*p, T, H, E, *o, int(accumulate), pw, nw), stream)
+    return out
+
+
+@_allocates
+def moe_ckpt_pack(x, out=None, stream=None):
+    """x [T,K] bf16 (rows may be strided) -> (codes [T,K], scales [T,K/128]) uint8."""
+    T, K = _matrix(x, "x")
+    dev = x.device
+    if out is None:
+        out = (torch.empty((T, K), dtype=torch.uint8, device=dev),
+               torch.empty((T, K // 128), dtype=torch.uint8, device=dev))
+    codes, scales = out
+    px = _arg(x, "x", torch.bfloat16, (T, K), dev, strided=True)
+    o = (_arg(codes, "codes", torch.uint8, (T, K), dev), _arg(scales, "scales", torch.uint8, (T, K // 128), dev))
+    _call(dev, lib.moe_ckpt_pack, (px, _row_stride(x), T, K, *o), stream)
+    return out
+
+
+@_allocates
+def moe_ckpt_unpack(codes, scales, out=None, stream=None):
+    """The activation a checkpoint holds, [T,K] bf16 (`out`'s rows may be strided)."""
+    T, K = _matrix(codes, "codes")
+    dev = codes.device
+    if out is None:
+        out = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+    p = (_arg(codes, "codes", torch.uint8, (T, K), dev), _arg(scales, "scales", torch.uint8, (T, K // 128), dev))
+    po = _arg(out, "out", torch.bfloat16, (T, K), dev, strided=True)
+    _call(dev, lib.moe_ckpt_unpack, (*p, T, K, po, _row_stride(out)), stream)
+    return out
+
+
+@_allocates
+def moe_ckpt_swiglu_backward(gu_codes, gu_scales, dh, need_h: bool = False, out=None, stream=None):
+    """Checkpoint of the gate|up activations [T,2I], dh [T,I] bf16 (rows may be
+    strided) -> (dgu [T,2I] bf16, h [T,I] bf16 or None)."""
+    T, I = _matrix(dh, "dh")
+    dev = dh.device
+    if out is None:
+        out = (torch.empty((T, 2 * I), dtype=torch.bfloat16, device=dev),
+               torch.empty((T, I), dtype=torch.bfloat16, device=dev) if need_h else None)
+    dgu, h = out
+    if need_h and h is None:
+        _bad("out holds no tensor for h")
+    p = (_arg(gu_codes, "gu_codes", torch.uint8, (T, 2 * I), dev),
+         _arg(gu_scales, "gu_scales", torch.uint8, (T, 2 * I // 128), dev),
+         _arg(dh, "dh", torch.bfloat16, (T, I), dev, strided=True), _row_stride(dh), T, I,
+         _arg(dgu, "dgu", torch.bfloat16, (T, 2 * I), dev),
+         _arg(h, "h", torch.bfloat16, (T, I), dev) if need_h else None)
+    _call(dev, lib.moe_ckpt_swiglu_backward, p, stream)
+    return dgu, (h if need_h else None)
+
+
+def moe_ckpt_wgrad_workspace_bytes(R_max: int, N: int, K: int, G: int = 1) -> int:
+    n = lib.moe_ckpt_wgrad_workspace_bytes(R_max, N, K, G)
+    if n == 0:
+        raise MoeError(-2, "unsupported dims")
+    return n
+
+
+@_allocates
+def moe_ckpt_wgrad(dy, codes, scales, offsets=None, perm=None, k: int = 1, dw=None, accumulate: bool = False, ws=None,
+                   stream=None):
+    """dy [R,N] bf16 (rows may be strided) and a checkpoint of x [X,K] -> the
+    weight gradient [N,K] fp32, or with offsets [G+1] int32 one per group
+    [G,N,K]; perm [R] int32 and k: row i of dy meets row perm[i] // k of x."""
+    R, N = _matrix(dy, "dy")
+    X, K = _matrix(codes, "codes")
+    dev = dy.device
+    G = 1 if offsets is None else offsets.numel() - 1
+    shape = (N, K) if offsets is None else (G, N, K)
+    if dw is None:
+        if accumulate:
+            _bad("accumulate needs dw")
+        dw = torch.empty(tuple(max(0, n) for n in shape), dtype=torch.float32, device=dev)
+    p = (_arg(dy, "dy", torch.bfloat16, (R, N), dev, strided=True), _row_stride(dy),
+         _arg(codes, "codes", torch.uint8, (X, K), dev), _arg(scales, "scales", torch.uint8, (X, K // 128), dev),
+         _arg(offsets, "offsets", torch.int32, (G + 1,), dev), _arg(perm, "perm", torch.int32, (R,), dev))
+    pd = _arg(dw, "dw", torch.float32, shape, dev)
+    ws, pw, nw = _ws_arg(ws, lib.moe_ckpt_wgrad_workspace_bytes(R, N, K, G), dev)
+    _call(dev, lib.moe_ckpt_wgrad, (*p, k, R, X, N, K, G, pd, int(accumulate), pw, nw), stream)
+    return dw
 
 
 MOE_OPT_TC_MIN_ROWS = 1

@@ -638,6 +638,188 @@ int moe_fp8_linear(const void* x_bf16, int T, int N, int K, const void* packed, 
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_fp8_linear launch");
 }
 
+// ---- Training: balance loss, gradients, 8-bit checkpoints ----------------------
+
+static int check_balance_dims(int T, int E, int k, int S, bool has_seq, const char* who) {
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T < 0", who);
+    if (E < 1 || E > 1024) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: E must be in [1, 1024] (got %d)", who, E);
+    if (k < 1 || k > 16 || k > E)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: k must be in [1, min(E, 16)] (got %d)", who, k);
+    if (S < 1 || S > 65535) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: S must be in [1, 65535] (got %d)", who, S);
+    if (!has_seq && S != 1) return fail(MOE_ERR_INVALID_ARG, "%s: S must be 1 without seq_offsets (got %d)", who, S);
+    return MOE_OK;
+}
+
+size_t moe_balance_workspace_bytes(int T_max, int E, int S_max) {
+    if (T_max < 0 || E < 1 || E > 1024 || S_max < 1 || S_max > 65535) return 0;
+    return moe::balance_workspace_bytes(T_max, E, S_max);
+}
+
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, const int32_t* seq_offsets,
+                     const uint8_t* token_mask, int T, int E, int k, int S, float coef, int32_t* counts,
+                     float* mean_prob, int32_t* tokens, float* loss, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    g_last_error.clear();
+    if (int rc = check_balance_dims(T, E, k, S, seq_offsets != nullptr, "moe_balance_loss")) return rc;
+    if (!counts || !tokens || !loss || !ws || (T > 0 && (!logits || !topk_idx)))
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: NULL pointer");
+    if (!aligned(ws, 256) || !aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(seq_offsets, 4) ||
+        !aligned(counts, 4) || !aligned(mean_prob, 4) || !aligned(tokens, 4) || !aligned(loss, 4))
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: ws needs 256-byte, the tensors 4-byte alignment");
+    if (ws_bytes < moe::balance_workspace_bytes(T, E, S))
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: ws_bytes %zu < %zu", ws_bytes,
+                    moe::balance_workspace_bytes(T, E, S));
+    cudaError_t e = moe::launch_balance_loss(logits, topk_idx, seq_offsets, token_mask, T, E, k, S, coef, counts,
+                                             mean_prob, tokens, loss, ws, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_balance_loss launch");
+}
+
+int moe_route_backward(const float* logits, const int32_t* topk_idx, const float* gates, const float* dgates,
+                       const float* dloss, const int32_t* counts, const int32_t* tokens, const int32_t* seq_offsets,
+                       const uint8_t* token_mask, int T, int E, int k, int S, float coef, float* dlogits,
+                       int32_t* flag, cudaStream_t stream) {
+    g_last_error.clear();
+    if (int rc = check_balance_dims(T, E, k, S, seq_offsets != nullptr, "moe_route_backward")) return rc;
+    if (T > 0 && !dgates && !dloss)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: dgates and dloss are both NULL");
+    if (T > 0 && (!logits || !dlogits || (dgates && (!gates || !topk_idx)) || (dloss && (!counts || !tokens))))
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: NULL pointer");
+    if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(gates, 4) || !aligned(dgates, 4) ||
+        !aligned(dloss, 4) || !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(seq_offsets, 4) ||
+        !aligned(dlogits, 4) || !aligned(flag, 4))
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: the tensors need 4-byte alignment");
+    const size_t bytes = 4 * (size_t)T * E;
+    if (T > 0 && (const char*)logits < (const char*)dlogits + bytes && (const char*)dlogits < (const char*)logits + bytes)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: dlogits overlaps logits");
+    cudaError_t e = moe::launch_route_backward(logits, topk_idx, gates, dgates, dloss, counts, tokens, seq_offsets,
+                                               token_mask, T, E, k, S, coef, dlogits, flag, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_route_backward launch");
+}
+
+size_t moe_router_backward_workspace_bytes(int T_max, int H, int E) {
+    if (T_max < 0 || H <= 0 || H % 32 || E < 1 || E > 1024) return 0;
+    return moe::router_backward_workspace_bytes(T_max, H, E);
+}
+
+int moe_router_logits_backward(const float* dlogits, const void* x_bf16, const uint8_t* x_codes,
+                               const uint8_t* x_scales, const float* w_router, int T, int H, int E, void* dx_bf16,
+                               float* dw, float* dbias, int accumulate, void* ws, size_t ws_bytes,
+                               cudaStream_t stream) {
+    g_last_error.clear();
+    const char* who = "moe_router_logits_backward";
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T < 0", who);
+    if (H <= 0 || H % 32) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H must be a positive multiple of 32 (got %d)", who, H);
+    if (E < 1 || E > 1024) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: E must be in [1, 1024] (got %d)", who, E);
+    if (accumulate != 0 && accumulate != 1) return fail(MOE_ERR_INVALID_ARG, "%s: accumulate must be 0 or 1", who);
+    if (!dx_bf16 && !dw && !dbias) return fail(MOE_ERR_INVALID_ARG, "%s: dx, dw and dbias are all NULL", who);
+    if (!ws || (T > 0 && !dlogits)) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (x_bf16 && (x_codes || x_scales)) return fail(MOE_ERR_INVALID_ARG, "%s: x in bf16 and as a checkpoint", who);
+    if ((x_codes != nullptr) != (x_scales != nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "%s: a checkpoint needs codes and scales", who);
+    if (x_codes && H % 128)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H must be a multiple of 128 with a checkpoint (got %d)", who, H);
+    if (T > 0 && dw && !x_bf16 && !x_codes) return fail(MOE_ERR_INVALID_ARG, "%s: dw needs x", who);
+    if (T > 0 && dx_bf16 && !w_router) return fail(MOE_ERR_INVALID_ARG, "%s: dx needs w_router", who);
+    if (!aligned(ws, 256) || !aligned(dlogits, 16) || !aligned(x_bf16, 16) || !aligned(x_codes, 16) ||
+        !aligned(w_router, 16) || !aligned(dx_bf16, 16) || !aligned(dw, 16) || !aligned(dbias, 4))
+        return fail(MOE_ERR_INVALID_ARG, "%s: ws needs 256-byte, the tensors 16-byte alignment", who);
+    if (ws_bytes < moe::router_backward_workspace_bytes(T, H, E))
+        return fail(MOE_ERR_INVALID_ARG, "%s: ws_bytes %zu < %zu", who, ws_bytes,
+                    moe::router_backward_workspace_bytes(T, H, E));
+    cudaError_t e = moe::launch_router_backward(dlogits, x_bf16, x_codes, x_scales, w_router, T, H, E, dx_bf16, dw,
+                                                dbias, accumulate, ws, load_options().wait_ns, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, who);
+}
+
+static int check_ckpt_dims(int T, int K, const char* who) {
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative number of rows", who);
+    if (K <= 0 || K % 128 || K > (1 << 24))
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: the row length must be a positive multiple of 128 (got %d)", who, K);
+    return MOE_OK;
+}
+static int check_stride(int64_t ld, int cols, const char* who) {
+    if (ld < cols || ld % 8 || ld > (1LL << 32))
+        return fail(MOE_ERR_INVALID_ARG, "%s: the row stride must be a multiple of 8 and at least %d (got %lld)", who,
+                    cols, (long long)ld);
+    return MOE_OK;
+}
+
+int moe_ckpt_pack(const void* x_bf16, int64_t ldx, int T, int K, uint8_t* codes, uint8_t* scales,
+                  cudaStream_t stream) {
+    g_last_error.clear();
+    if (int rc = check_ckpt_dims(T, K, "moe_ckpt_pack")) return rc;
+    if (int rc = check_stride(ldx, K, "moe_ckpt_pack")) return rc;
+    if (T > 0 && (!x_bf16 || !codes || !scales)) return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_pack: NULL pointer");
+    if (!aligned(x_bf16, 16) || !aligned(codes, 16))
+        return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_pack: x and codes need 16-byte alignment");
+    cudaError_t e = moe::launch_ckpt_pack(x_bf16, ldx, T, K, codes, scales, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_ckpt_pack launch");
+}
+
+int moe_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int T, int K, void* x_bf16, int64_t ldx,
+                    cudaStream_t stream) {
+    g_last_error.clear();
+    if (int rc = check_ckpt_dims(T, K, "moe_ckpt_unpack")) return rc;
+    if (int rc = check_stride(ldx, K, "moe_ckpt_unpack")) return rc;
+    if (T > 0 && (!x_bf16 || !codes || !scales)) return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_unpack: NULL pointer");
+    if (!aligned(x_bf16, 16) || !aligned(codes, 16))
+        return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_unpack: x and codes need 16-byte alignment");
+    cudaError_t e = moe::launch_ckpt_unpack(codes, scales, T, K, x_bf16, ldx, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_ckpt_unpack launch");
+}
+
+int moe_ckpt_swiglu_backward(const uint8_t* gu_codes, const uint8_t* gu_scales, const void* dh_bf16, int64_t lddh,
+                             int T, int I, void* dgu_bf16, void* h_bf16, cudaStream_t stream) {
+    g_last_error.clear();
+    const char* who = "moe_ckpt_swiglu_backward";
+    if (int rc = check_ckpt_dims(T, I, who)) return rc;
+    if (int rc = check_stride(lddh, I, who)) return rc;
+    if (T > 0 && (!gu_codes || !gu_scales || !dh_bf16 || !dgu_bf16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (!aligned(gu_codes, 16) || !aligned(dh_bf16, 16) || !aligned(dgu_bf16, 16) || !aligned(h_bf16, 16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: codes, dh, dgu and h need 16-byte alignment", who);
+    cudaError_t e = moe::launch_ckpt_swiglu_backward(gu_codes, gu_scales, dh_bf16, lddh, T, I, dgu_bf16, h_bf16, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, who);
+}
+
+static bool wgrad_dims_ok(int R, int N, int K, int G) {
+    return R >= 0 && N > 0 && N % 8 == 0 && N <= (1 << 20) && K > 0 && K % 128 == 0 && K <= (1 << 20) && G >= 1 &&
+           G <= 1024;
+}
+
+size_t moe_ckpt_wgrad_workspace_bytes(int R_max, int N, int K, int G) {
+    if (!wgrad_dims_ok(R_max, N, K, G)) return 0;
+    return moe::wgrad_workspace_bytes(R_max, N, K, G);
+}
+
+int moe_ckpt_wgrad(const void* dy_bf16, int64_t lddy, const uint8_t* x_codes, const uint8_t* x_scales,
+                   const int32_t* offsets, const int32_t* perm, int k_div, int R, int X, int N, int K, int G,
+                   float* dw, int accumulate, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    g_last_error.clear();
+    const char* who = "moe_ckpt_wgrad";
+    if (R < 0 || X < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative number of rows", who);
+    if (!wgrad_dims_ok(R, N, K, G))
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE,
+                    "%s: N must be a multiple of 8, K of 128 (both at most 2^20), G in [1, 1024] (N=%d K=%d G=%d)",
+                    who, N, K, G);
+    if (!offsets && G != 1) return fail(MOE_ERR_INVALID_ARG, "%s: G must be 1 without offsets (got %d)", who, G);
+    if (accumulate != 0 && accumulate != 1) return fail(MOE_ERR_INVALID_ARG, "%s: accumulate must be 0 or 1", who);
+    if (int rc = check_stride(lddy, N, who)) return rc;
+    if (!dw || !ws || (R > 0 && (!dy_bf16 || !x_codes || !x_scales)))
+        return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (perm && k_div < 1) return fail(MOE_ERR_INVALID_ARG, "%s: k_div must be at least 1 (got %d)", who, k_div);
+    if (perm ? (R > 0 && X < 1) : X < R)
+        return fail(MOE_ERR_INVALID_ARG, "%s: the checkpoint has %d rows for %d", who, X, R);
+    if (!aligned(ws, 256) || !aligned(dy_bf16, 16) || !aligned(x_codes, 16) || !aligned(dw, 16) ||
+        !aligned(offsets, 4) || !aligned(perm, 4))
+        return fail(MOE_ERR_INVALID_ARG, "%s: ws needs 256-byte, dy, codes and dw 16-byte alignment", who);
+    if (ws_bytes < moe::wgrad_workspace_bytes(R, N, K, G))
+        return fail(MOE_ERR_INVALID_ARG, "%s: ws_bytes %zu < %zu", who, ws_bytes,
+                    moe::wgrad_workspace_bytes(R, N, K, G));
+    cudaError_t e = moe::launch_ckpt_wgrad(dy_bf16, lddy, x_codes, x_scales, offsets, perm, k_div, R, X, N, K, G, dw,
+                                           accumulate, ws, load_options().wait_ns, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, who);
+}
+
 unsigned long long moe_launch_count(void) { return moe::g_launches.load(); }
 
 int moe_set_option(int option, int value) {

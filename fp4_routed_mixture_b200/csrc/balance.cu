@@ -1,0 +1,497 @@
+// Load-balance loss of the router with its per-expert counts, and the gradient
+// of the logits (formulas at moe_balance_loss and moe_route_backward in the
+// header).
+//
+//   k_balance_rows    softmax of every row; per chunk of rows and sequence the
+//                     sum of the probabilities, the counts and the valid tokens
+//   k_balance_reduce  adds the chunks of each sequence in a fixed order, forms
+//                     f and P, and (last CTA) the loss
+//   k_route_backward  one pass: recomputes each row's softmax and writes the
+//                     gradient of the balance loss and of the gates
+//
+// A chunk c of rows and a sequence s that meet own slot c + s of the
+// workspace: walking the rows, every step to the next (chunk, sequence) pair
+// raises c, s or both, so the sum is unique, and chunks + S slots are enough
+// for any ragged split.  No atomics on floating-point values: results do not
+// depend on the order in which CTAs run.
+// All three read [T, E] once (the backward also writes it): HBM bound.
+#include "kernels.cuh"
+#include "moe_common.cuh"
+
+namespace moe {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBalMaxChunks = 148 * 4;
+
+struct BalanceWs {
+    size_t meta, prob, hits, part, total;
+    int slots;
+};
+
+static int bal_chunk_rows(int T) {
+    return std::max(kBalWarps, (int)align_up((size_t)(T + kBalMaxChunks - 1) / kBalMaxChunks, kBalWarps));
+}
+
+static BalanceWs balance_ws(int T, int E, int S) {
+    BalanceWs L;
+    // (the chunk count is not monotonic in T; this bound is)
+    const int chunks = std::min(kBalMaxChunks, (T + kBalWarps - 1) / kBalWarps);
+    L.slots = chunks + S;
+    size_t o = 256;   // error word, arrival counter
+    L.meta = o; o += align_up(sizeof(int2) * (size_t)L.slots, 256);
+    L.prob = o; o += align_up(sizeof(float) * (size_t)L.slots * E, 256);
+    L.hits = o; o += align_up(sizeof(int) * (size_t)L.slots * E, 256);
+    L.part = o; o += align_up(sizeof(float) * (size_t)S * ((E + 31) / 32), 256);
+    L.total = o;
+    return L;
+}
+
+size_t balance_workspace_bytes(int T, int E, int S) { return balance_ws(T, E, S).total; }
+
+// Sequence bounds read from the caller's table (NULL: one sequence of T rows),
+// clamped so that a bad table cannot lead out of the tensors.
+struct SeqTable {
+    const int32_t* off;
+    int T, S;
+    __device__ int at(int s) const {
+        if (!off) return s == 0 ? 0 : T;
+        return min(max(__ldg(off + s), 0), T);
+    }
+    // the first sequence that ends behind row r (S when none does)
+    __device__ int find(int r) const {
+        int lo = 0, hi = S;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (at(mid + 1) > r) hi = mid; else lo = mid + 1;
+        }
+        return lo;
+    }
+};
+
+// Column of a lane's value v: four neighbours per 128 columns (VEC, one
+// 16-byte access) or every 32nd column.
+template <bool VEC>
+__device__ __forceinline__ int bal_col(int v, int lane) {
+    return VEC ? ((v >> 2) * 128 + lane * 4 + (v & 3)) : (v * 32 + lane);
+}
+
+template <int N, bool VEC>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int lane, float (&x)[N]) {
+    if (VEC) {
+#pragma unroll
+        for (int v = 0; v < N; v += 4) {
+            const int c = bal_col<true>(v, lane);
+            float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (c < E) q = __ldg(reinterpret_cast<const float4*>(row + c));
+            x[v] = q.x; x[v + 1] = q.y; x[v + 2] = q.z; x[v + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+            const int c = bal_col<false>(v, lane);
+            x[v] = c < E ? __ldg(row + c) : -INFINITY;
+        }
+    }
+}
+
+// x <- softmax of the row the warp holds (columns behind E hold -inf and get
+// 0).  A row of -inf alone has no distribution: its probabilities are 0.  The
+// exponent is taken after the maximum is subtracted, the sum is fp32.
+template <int N>
+__device__ __forceinline__ void row_softmax(float (&x)[N]) {
+    float m = x[0];
+    bool nan = false;
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+        m = fmaxf(m, x[v]);
+        nan |= x[v] != x[v];
+    }
+    m = warp_max(m);
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+        x[v] = expf(x[v] - m);       // (+inf - +inf and NaN rows: NaN)
+        sum += x[v];
+    }
+    sum = warp_sum(sum);
+    nan = __any_sync(0xffffffffu, nan);
+    const float inv = (m == -INFINITY && !nan) ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int v = 0; v < N; ++v) x[v] = (m == -INFINITY && !nan) ? 0.0f : x[v] * inv;
+}
+
+struct BalanceArgs {
+    const float* logits;
+    const int32_t* idx;
+    const uint8_t* mask;
+    SeqTable seq;
+    int T, E, k, rows;      // rows per chunk
+    int32_t* head;          // error word, arrival counter
+    int2* meta;             // per slot: valid tokens, error bits
+    float* prob;            // [slots, E]
+    int* hits;              // [slots, E]
+};
+
+template <int N, bool VEC>
+__global__ void __launch_bounds__(kBalThreads) k_balance_rows(BalanceArgs a) {
+    pdl_begin();
+    extern __shared__ float bal_smem[];
+    float* sp = bal_smem;                                   // [warps][E]
+    int* sc = reinterpret_cast<int*>(bal_smem + kBalWarps * a.E);   // [E]
+    __shared__ int s_n, s_bad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = a.head[1] = 0;
+    const int r0 = blockIdx.x * a.rows, r1 = min(a.T, r0 + a.rows);
+    for (int s = a.seq.find(r0); s < a.seq.S; ++s) {
+        const int b = max(a.seq.at(s), r0), e = min(a.seq.at(s + 1), r1);
+        if (a.seq.at(s) >= r1) break;
+        if (e <= b) continue;
+        for (int c = threadIdx.x; c < a.E; c += kBalThreads) sc[c] = 0;
+        if (threadIdx.x == 0) s_n = s_bad = 0;
+        __syncthreads();
+        float acc[N] = {};
+        float nx[N];
+        if (b + warp < e) load_row<N, VEC>(a.logits + (size_t)(b + warp) * a.E, a.E, lane, nx);
+        int n = 0;
+        for (int r = b + warp; r < e; r += kBalWarps) {
+            float x[N];
+#pragma unroll
+            for (int v = 0; v < N; ++v) x[v] = nx[v];
+            if (r + kBalWarps < e) load_row<N, VEC>(a.logits + (size_t)(r + kBalWarps) * a.E, a.E, lane, nx);
+            if (a.mask && !__ldg(a.mask + r)) continue;
+            ++n;
+            row_softmax<N>(x);
+#pragma unroll
+            for (int v = 0; v < N; ++v) acc[v] += x[v];
+            if (lane < a.k) {
+                const int id = __ldg(a.idx + (size_t)r * a.k + lane);
+                if ((unsigned)id < (unsigned)a.E)
+                    atomicAdd(sc + id, 1);
+                else
+                    s_bad = FLAG_BAD_EXPERT;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+            const int c = bal_col<VEC>(v, lane);
+            if (c < a.E) sp[warp * a.E + c] = acc[v];
+        }
+        if (lane == 0) atomicAdd(&s_n, n);
+        __syncthreads();
+        const size_t slot = (size_t)blockIdx.x + s;
+        for (int c = threadIdx.x; c < a.E; c += kBalThreads) {
+            float t = sp[c];
+#pragma unroll
+            for (int w = 1; w < kBalWarps; ++w) t += sp[w * a.E + c];
+            a.prob[slot * a.E + c] = t;
+            a.hits[slot * a.E + c] = sc[c];
+        }
+        if (threadIdx.x == 0) a.meta[slot] = make_int2(s_n, s_bad);
+        __syncthreads();
+    }
+}
+
+// CTA (column block of 32, sequence): 8 warps take every eighth chunk of the
+// sequence, lane = column; the eight sums are added in warp order.
+struct BalanceReduceArgs {
+    SeqTable seq;
+    int T, E, k, rows;
+    float coef;
+    int32_t* head;
+    const int2* meta;
+    const float* prob;
+    const int* hits;
+    float* part;            // [S][column blocks]
+    int32_t* counts;
+    float* mean_prob;       // or NULL
+    int32_t* tokens;        // [S + 1]
+    float* loss;
+};
+
+__global__ void __launch_bounds__(kBalThreads) k_balance_reduce(BalanceReduceArgs a) {
+    pdl_begin();
+    __shared__ float sp[kBalWarps][33];
+    __shared__ int sc[kBalWarps][33];
+    __shared__ int sn[kBalWarps];
+    __shared__ bool s_last;
+    __shared__ double sred[kBalWarps];
+    __shared__ int sused[kBalWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int CB = (a.E + 31) / 32, cb = blockIdx.x, s = blockIdx.y;
+    const int col = cb * 32 + lane;
+    const int b = a.seq.at(s), e = a.seq.at(s + 1);
+    if (a.seq.off && threadIdx.x == 0 && cb == 0) {
+        const int rb = __ldg(a.seq.off + s), re = __ldg(a.seq.off + s + 1);
+        if (rb < 0 || re > a.T || re < rb) raise_flag(a.head, FLAG_BOUNDS);
+    }
+    const int c0 = b / a.rows, c1 = e > b ? (e - 1) / a.rows + 1 : c0;
+    float p = 0.0f;
+    int h = 0, n = 0, bad = 0;
+    for (int c = c0 + warp; c < c1; c += kBalWarps) {
+        const size_t slot = (size_t)c + s;
+        const int2 m = a.meta[slot];
+        n += m.x;
+        bad |= m.y;
+        if (col < a.E) {
+            p += a.prob[slot * a.E + col];
+            h += a.hits[slot * a.E + col];
+        }
+    }
+    sp[warp][lane] = p;
+    sc[warp][lane] = h;
+    if (lane == 0) sn[warp] = n;
+    if (bad && lane == 0 && cb == 0) raise_flag(a.head, bad);
+    __syncthreads();
+    if (warp == 0) {
+        n = 0;
+        p = 0.0f;
+        h = 0;
+#pragma unroll
+        for (int w = 0; w < kBalWarps; ++w) {
+            n += sn[w];
+            p += sp[w][lane];
+            h += sc[w][lane];
+        }
+        float term = 0.0f;
+        if (col < a.E) {
+            const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+            const float mp = p * inv;
+            a.counts[(size_t)s * a.E + col] = h;
+            if (a.mean_prob) a.mean_prob[(size_t)s * a.E + col] = mp;
+            term = (float)h * ((float)a.E / (float)a.k * inv) * mp;
+        }
+        term = warp_sum(term);
+        if (lane == 0) {
+            a.part[(size_t)s * CB + cb] = term;
+            if (cb == 0) a.tokens[s] = n;
+            __threadfence();
+            s_last = atomicAdd(a.head + 1, 1) == (int)(gridDim.x * gridDim.y) - 1;
+        }
+    }
+    __syncthreads();
+    if (!s_last) return;
+    // the last CTA adds the terms (and counts the sequences in use) in a fixed order
+    __threadfence();
+    double sum = 0.0;
+    int used = 0;
+    const int total = a.seq.S * CB;
+    for (int i = threadIdx.x; i < total; i += kBalThreads) sum += (double)__ldcg(a.part + i);
+    for (int i = threadIdx.x; i < a.seq.S; i += kBalThreads) used += __ldcg(a.tokens + i) > 0;
+    sum = warp_sum(sum);
+    used = warp_sum(used);
+    if (lane == 0) {
+        sred[warp] = sum;
+        sused[warp] = used;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sum = 0.0;
+        used = 0;
+        for (int w = 0; w < kBalWarps; ++w) {
+            sum += sred[w];
+            used += sused[w];
+        }
+        a.tokens[a.seq.S] = used;
+        *a.loss = used > 0 ? (float)((double)a.coef * sum / (double)used) : 0.0f;
+    }
+}
+
+// No tokens: every output is zero.
+__global__ void k_balance_empty(int32_t* head, int32_t* counts, float* mean_prob, int32_t* tokens, float* loss,
+                                int E, int S) {
+    pdl_begin();
+    const size_t n = (size_t)S * E, i0 = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
+    for (size_t i = i0; i < n; i += (size_t)gridDim.x * blockDim.x) {
+        counts[i] = 0;
+        if (mean_prob) mean_prob[i] = 0.0f;
+    }
+    for (size_t i = i0; i <= (size_t)S; i += (size_t)gridDim.x * blockDim.x) tokens[i] = 0;
+    if (i0 == 0) {
+        *head = 0;
+        *loss = 0.0f;
+    }
+}
+
+// ---- gradient of the logits ----------------------------------------------------
+struct RouteBackwardArgs {
+    const float* logits;
+    const int32_t* idx;
+    const float* gates;
+    const float* dgates;    // or NULL
+    const float* dloss;     // or NULL
+    const int32_t* counts;
+    const int32_t* tokens;  // [S + 1]
+    const uint8_t* mask;
+    SeqTable seq;
+    int T, E, k, rows;      // rows per warp
+    float coef;
+    float* dlogits;
+    int32_t* flag;          // or NULL
+};
+
+// A warp takes `rows` consecutive rows, so that f of their sequence stays in
+// registers until the sequence changes.
+template <int N, bool VEC>
+__global__ void __launch_bounds__(kBalThreads) k_route_backward(RouteBackwardArgs a) {
+    pdl_begin();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long first = ((long long)blockIdx.x * kBalWarps + warp) * a.rows;
+    if (first >= a.T) return;
+    const int r0 = (int)first, r1 = (int)min((long long)a.T, first + a.rows);
+    int s = -1, s_end = r0;       // the sequence whose f is in registers ends at s_end
+    float f[N], w = 0.0f;
+    float nx[N];
+    load_row<N, VEC>(a.logits + (size_t)r0 * a.E, a.E, lane, nx);
+    for (int r = r0; r < r1; ++r) {
+        float x[N];
+#pragma unroll
+        for (int v = 0; v < N; ++v) x[v] = nx[v];
+        if (r + 1 < r1) load_row<N, VEC>(a.logits + (size_t)(r + 1) * a.E, a.E, lane, nx);
+        float add = 0.0f;
+        int id = -1;
+        if (a.dgates) {
+            float g = 0.0f, dg = 0.0f;
+            if (lane < a.k) {
+                id = __ldg(a.idx + (size_t)r * a.k + lane);
+                g = __ldg(a.gates + (size_t)r * a.k + lane);
+                dg = __ldg(a.dgates + (size_t)r * a.k + lane);
+                if ((unsigned)id >= (unsigned)a.E) {
+                    raise_flag(a.flag, FLAG_BAD_EXPERT);
+                    id = -1;
+                }
+            }
+            add = g * (dg - warp_sum(g * dg));
+        }
+        bool on = a.dloss && !(a.mask && !__ldg(a.mask + r));
+        if (on && r >= s_end) {
+            s = a.seq.find(r);
+            s_end = s < a.seq.S ? a.seq.at(s + 1) : a.T;
+            // rows in front of the first or behind the last sequence belong to none
+            const bool in = s < a.seq.S && a.seq.at(s) <= r;
+            const int n = in ? __ldg(a.tokens + s) : 0;
+            const int used = __ldg(a.tokens + a.seq.S);
+            w = 0.0f;
+            if (n > 0 && used > 0) {
+                const float inv = 1.0f / (float)n;
+                w = __ldg(a.dloss) * (a.coef / (float)used) * inv;
+                const float fs = (float)a.E / (float)a.k * inv;
+                const int32_t* cr = a.counts + (size_t)s * a.E;
+#pragma unroll
+                for (int v = 0; v < N; ++v) {
+                    const int c = bal_col<VEC>(v, lane);
+                    f[v] = c < a.E ? (float)__ldg(cr + c) * fs : 0.0f;
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < N; ++v) f[v] = 0.0f;
+                if (!in) s_end = min(s_end, r + 1);
+            }
+        }
+        if (on && w != 0.0f) {
+            row_softmax<N>(x);
+            float dot = 0.0f;
+#pragma unroll
+            for (int v = 0; v < N; ++v) dot = fmaf(x[v], f[v], dot);
+            dot = warp_sum(dot);
+#pragma unroll
+            for (int v = 0; v < N; ++v) x[v] = w * x[v] * (f[v] - dot);
+        } else {
+#pragma unroll
+            for (int v = 0; v < N; ++v) x[v] = 0.0f;
+        }
+        if (a.dgates) {
+            for (int j = 0; j < a.k; ++j) {
+                const int ij = __shfl_sync(0xffffffffu, id, j);
+                const float aj = __shfl_sync(0xffffffffu, add, j);
+#pragma unroll
+                for (int v = 0; v < N; ++v)
+                    if (bal_col<VEC>(v, lane) == ij) x[v] += aj;
+            }
+        }
+        float* out = a.dlogits + (size_t)r * a.E;
+        if (VEC) {
+#pragma unroll
+            for (int v = 0; v < N; v += 4) {
+                const int c = bal_col<true>(v, lane);
+                if (c < a.E) *reinterpret_cast<float4*>(out + c) = make_float4(x[v], x[v + 1], x[v + 2], x[v + 3]);
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                const int c = bal_col<false>(v, lane);
+                if (c < a.E) out[c] = x[v];
+            }
+        }
+    }
+}
+
+// Values per lane: E <= 32 N; the 16-byte form needs rows on 16-byte bounds.
+#define MOE_BAL_DISPATCH(E, vec, CALL)                       \
+    do {                                                     \
+        if (vec) {                                           \
+            if ((E) <= 128) { CALL(4, true); }               \
+            else if ((E) <= 256) { CALL(8, true); }          \
+            else if ((E) <= 512) { CALL(16, true); }         \
+            else { CALL(32, true); }                         \
+        } else {                                             \
+            if ((E) <= 64) { CALL(2, false); }               \
+            else if ((E) <= 256) { CALL(8, false); }         \
+            else { CALL(32, false); }                        \
+        }                                                    \
+    } while (0)
+
+static bool bal_vec(int E, const void* p, const void* q) {
+    return E % 4 == 0 && ((uintptr_t)p | (uintptr_t)q) % 16 == 0;
+}
+
+cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* seq_off, const uint8_t* mask,
+                                int T, int E, int k, int S, float coef, int32_t* counts, float* mean_prob,
+                                int32_t* tokens, float* loss, void* ws, cudaStream_t st) {
+    char* w = (char*)ws;
+    int32_t* head = (int32_t*)w;
+    cudaError_t e;
+    if (T == 0) {
+        e = launch_pdl(k_balance_empty, dim3((unsigned)std::min<size_t>(((size_t)S * E + 255) / 256 + 1, 592)), dim3(256), 0, st,
+                       head, counts, mean_prob, tokens, loss, E, S);
+        count_launches(1);
+        return e;
+    }
+    const BalanceWs L = balance_ws(T, E, S);
+    const SeqTable seq{seq_off, T, S};
+    const int rows = bal_chunk_rows(T);
+    BalanceArgs a{logits, idx, mask, seq, T, E, k, rows, head, (int2*)(w + L.meta), (float*)(w + L.prob),
+                  (int*)(w + L.hits)};
+    const dim3 grid((unsigned)((T + rows - 1) / rows));
+    const size_t smem = (size_t)(kBalWarps + 1) * E * 4;      // at most 36 KB
+#define MOE_BAL_CALL(N, V) e = launch_pdl(k_balance_rows<N, V>, grid, dim3(kBalThreads), smem, st, a)
+    MOE_BAL_DISPATCH(E, bal_vec(E, logits, logits), MOE_BAL_CALL);
+#undef MOE_BAL_CALL
+    count_launches(1);
+    if (e != cudaSuccess) return e;
+    BalanceReduceArgs b{seq, T, E, k, rows, coef, head, (const int2*)(w + L.meta), (const float*)(w + L.prob),
+                        (const int*)(w + L.hits), (float*)(w + L.part), counts, mean_prob, tokens, loss};
+    e = launch_pdl(k_balance_reduce, dim3((unsigned)((E + 31) / 32), (unsigned)S), dim3(kBalThreads), 0, st, b);
+    count_launches(1);
+    return e;
+}
+
+cudaError_t launch_route_backward(const float* logits, const int32_t* idx, const float* gates, const float* dgates,
+                                  const float* dloss, const int32_t* counts, const int32_t* tokens,
+                                  const int32_t* seq_off, const uint8_t* mask, int T, int E, int k, int S, float coef,
+                                  float* dlogits, int32_t* flag, cudaStream_t st) {
+    if (T == 0) return cudaSuccess;
+    // one row per warp until the SMs are full, then up to 8
+    const int rows = std::min(8, std::max(1, T / (148 * 32)));
+    RouteBackwardArgs a{logits, idx, gates, dgates, dloss, counts, tokens, mask, SeqTable{seq_off, T, S}, T, E, k,
+                        rows, coef, dlogits, flag};
+    const dim3 grid((unsigned)((T + rows * kBalWarps - 1) / (rows * kBalWarps)));
+    cudaError_t e;
+#define MOE_BAL_CALL(N, V) e = launch_pdl(k_route_backward<N, V>, grid, dim3(kBalThreads), 0, st, a)
+    MOE_BAL_DISPATCH(E, bal_vec(E, logits, dlogits), MOE_BAL_CALL);
+#undef MOE_BAL_CALL
+    count_launches(1);
+    return e;
+}
+
+}  // namespace moe

@@ -1,0 +1,203 @@
+// 8-bit activation checkpoints (format: ckpt.cuh) and the SwiGLU gradient that
+// reads its inputs from one.  All three kernels stream: HBM bound.
+#include "ckpt.cuh"
+#include "kernels.cuh"
+#include "moe_common.cuh"
+
+namespace moe {
+
+constexpr int kCkThreads = 256;
+
+// Items of 8 inputs, 16 neighbouring lanes to a 128-input block: every load
+// and store of a warp is one contiguous piece.  Each thread takes kCkUnroll
+// items, a grid stride apart, and issues their loads together.
+constexpr int kCkUnroll = 4;
+
+__global__ void __launch_bounds__(kCkThreads)
+    k_ckpt_pack(const __nv_bfloat16* __restrict__ x, long long ldx, long long items, int K8,
+                uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+    pdl_begin();
+    const long long stride = (long long)gridDim.x * kCkThreads;
+    // (items and stride are multiples of 16: the lanes of a block agree)
+    for (long long i0 = blockIdx.x * (long long)kCkThreads + threadIdx.x; i0 - (threadIdx.x & 31) < items; i0 += stride * kCkUnroll) {
+        uint4 q[kCkUnroll];
+#pragma unroll
+        for (int u = 0; u < kCkUnroll; ++u) {
+            const long long i = i0 + u * stride;
+            q[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < items) {
+                const long long t = i / K8;
+                q[u] = __ldg(reinterpret_cast<const uint4*>(x + t * ldx + (i - t * K8) * 8));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kCkUnroll; ++u) {
+            const long long i = i0 + u * stride;
+            float v[8];
+            bf16x8_values(q[u], v);
+            float amax = 0.0f;
+            uint32_t bad = 0;        // bit j: value j is a NaN or an infinity
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float a = fabsf(v[j]);
+                if (a <= 3.4028235e38f)
+                    amax = fmaxf(amax, a);
+                else
+                    bad |= 1u << j;
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (i >= items) continue;
+            const int e = ckpt_exponent(amax);
+            const float inv = ckpt_pow2(-e);
+            const float top = e >= 120 ? 240.0f : 448.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = fminf(fmaxf(v[j] * inv, -top), top);
+            uint2 c = make_uint2(e4m3x4_code(v[0], v[1], v[2], v[3]), e4m3x4_code(v[4], v[5], v[6], v[7]));
+            if (bad) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (bad >> j & 1u) {
+                        uint32_t& w = j < 4 ? c.x : c.y;
+                        w = (w & ~(0xffu << (8 * (j & 3)))) | (0x7fu << (8 * (j & 3)));
+                    }
+            }
+            *reinterpret_cast<uint2*>(codes + i * 8) = c;
+            if ((i & 15) == 0) scales[i >> 4] = (uint8_t)(e + 127);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kCkThreads)
+    k_ckpt_unpack(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long items, int K8,
+                  __nv_bfloat16* __restrict__ x, long long ldx) {
+    pdl_begin();
+    const long long stride = (long long)gridDim.x * kCkThreads;
+    for (long long i0 = blockIdx.x * (long long)kCkThreads + threadIdx.x; i0 < items; i0 += stride * kCkUnroll) {
+        uint2 c[kCkUnroll];
+        uint32_t s[kCkUnroll];
+#pragma unroll
+        for (int u = 0; u < kCkUnroll; ++u) {
+            const long long i = i0 + u * stride;
+            if (i < items) {
+                c[u] = __ldg(reinterpret_cast<const uint2*>(codes + i * 8));
+                s[u] = __ldg(scales + (i >> 4));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kCkUnroll; ++u) {
+            const long long i = i0 + u * stride;
+            if (i >= items) break;
+            float v[8];
+            ckpt_values8(c[u], ckpt_scale(s[u]), v);
+            const long long t = i / K8;
+            *reinterpret_cast<uint4*>(x + t * ldx + (i - t * K8) * 8) = bf16x8_rn(v);
+        }
+    }
+}
+
+// SwiGLU: h = g s(g) u with s the logistic function, so
+//   dg = dh u (s + g s (1 - s)),  du = dh g s.
+// One item is 8 neighbouring features of a row: 8 + 8 code bytes, 16 bytes of
+// dh, and 16 bytes each of dg, du and (H) h.  fp32 throughout, one rounding
+// per output.  s and 1 - s are both quotients of non-negative terms,
+// 1 / (1 + e^-|g|) and e^-|g| / (1 + e^-|g|) in turn, so neither cancels.
+template <bool H>
+__global__ void __launch_bounds__(kCkThreads)
+    k_ckpt_swiglu_bwd(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                      const __nv_bfloat16* __restrict__ dh, long long lddh, long long items, int I,
+                      __nv_bfloat16* __restrict__ dgu, __nv_bfloat16* __restrict__ h) {
+    pdl_begin();
+    constexpr int U = 2;
+    const int I8 = I / 8, KB = I / 128;
+    const long long stride = (long long)gridDim.x * kCkThreads;
+    for (long long i0 = blockIdx.x * (long long)kCkThreads + threadIdx.x; i0 < items; i0 += stride * U) {
+        uint2 cg[U], cu[U];
+        uint32_t sg[U], su[U];
+        uint4 d[U];
+        long long t[U];
+        int c8[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long i = i0 + u * stride;
+            if (i < items) {
+                t[u] = i / I8;
+                c8[u] = (int)(i - t[u] * I8);
+                const uint8_t* row = codes + t[u] * 2 * I + c8[u] * 8;
+                const uint8_t* srow = scales + t[u] * 2 * KB + (c8[u] >> 4);
+                cg[u] = __ldg(reinterpret_cast<const uint2*>(row));
+                cu[u] = __ldg(reinterpret_cast<const uint2*>(row + I));
+                sg[u] = __ldg(srow);
+                su[u] = __ldg(srow + KB);
+                d[u] = __ldg(reinterpret_cast<const uint4*>(dh + t[u] * lddh + c8[u] * 8));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u * stride >= items) break;
+            float g[8], up[8], dv[8], og[8], ou[8], oh[8];
+            ckpt_values8(cg[u], ckpt_scale(sg[u]), g);
+            ckpt_values8(cu[u], ckpt_scale(su[u]), up);
+            bf16x8_values(d[u], dv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float e = __expf(-fabsf(g[j]));
+                const float r = __fdividef(1.0f, 1.0f + e);
+                const float er = e * r;
+                const float s = g[j] >= 0.0f ? r : er;       // NaN: er, a NaN
+                const float q = g[j] >= 0.0f ? er : r;       // 1 - s
+                const float a = g[j] * s;
+                og[j] = dv[j] * up[j] * fmaf(a, q, s);
+                ou[j] = dv[j] * a;
+                oh[j] = a * up[j];
+            }
+            __nv_bfloat16* o = dgu + t[u] * 2 * I + c8[u] * 8;
+            *reinterpret_cast<uint4*>(o) = bf16x8_rn(og);
+            *reinterpret_cast<uint4*>(o + I) = bf16x8_rn(ou);
+            if (H) *reinterpret_cast<uint4*>(h + t[u] * I + c8[u] * 8) = bf16x8_rn(oh);
+        }
+    }
+}
+
+static dim3 ck_grid(long long items, int per_thread) {
+    const long long ctas = (items + (long long)kCkThreads * per_thread - 1) / ((long long)kCkThreads * per_thread);
+    return dim3((unsigned)std::max(1LL, std::min(ctas, 148LL * 64)));
+}
+
+cudaError_t launch_ckpt_pack(const void* x, long long ldx, int T, int K, uint8_t* codes, uint8_t* scales,
+                             cudaStream_t st) {
+    if (T == 0) return cudaSuccess;
+    const long long items = (long long)T * (K / 8);
+    const cudaError_t e = launch_pdl(k_ckpt_pack, ck_grid(items, kCkUnroll), dim3(kCkThreads), 0, st,
+                                     (const __nv_bfloat16*)x, ldx, items, K / 8, codes, scales);
+    count_launches(1);
+    return e;
+}
+
+cudaError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int T, int K, void* x, long long ldx,
+                               cudaStream_t st) {
+    if (T == 0) return cudaSuccess;
+    const long long items = (long long)T * (K / 8);
+    const cudaError_t e = launch_pdl(k_ckpt_unpack, ck_grid(items, kCkUnroll), dim3(kCkThreads), 0, st, codes, scales,
+                                     items, K / 8, (__nv_bfloat16*)x, ldx);
+    count_launches(1);
+    return e;
+}
+
+cudaError_t launch_ckpt_swiglu_backward(const uint8_t* codes, const uint8_t* scales, const void* dh, long long lddh,
+                                        int T, int I, void* dgu, void* h, cudaStream_t st) {
+    if (T == 0) return cudaSuccess;
+    const long long items = (long long)T * (I / 8);
+    const dim3 grid = ck_grid(items, 2);
+    cudaError_t e;
+    if (h)
+        e = launch_pdl(k_ckpt_swiglu_bwd<true>, grid, dim3(kCkThreads), 0, st, codes, scales, (const __nv_bfloat16*)dh,
+                       lddh, items, I, (__nv_bfloat16*)dgu, (__nv_bfloat16*)h);
+    else
+        e = launch_pdl(k_ckpt_swiglu_bwd<false>, grid, dim3(kCkThreads), 0, st, codes, scales,
+                       (const __nv_bfloat16*)dh, lddh, items, I, (__nv_bfloat16*)dgu, (__nv_bfloat16*)h);
+    count_launches(1);
+    return e;
+}
+
+}  // namespace moe

@@ -214,4 +214,30 @@ cudaError_t launch_fp8_pack(int N, int K, const uint8_t* wq, const uint8_t* ws, 
 cudaError_t launch_fp8_linear(const void* x, int T, int N, int K, const void* packed, void* y, void* ws,
                               uint8_t* dbg_q, uint8_t* dbg_s, uint64_t wait_ns, cudaStream_t st);
 
+// ---- Training: balance loss and the logits' gradient (balance.cu) ----
+size_t balance_workspace_bytes(int T, int E, int S);
+cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* seq_off, const uint8_t* mask,
+                                int T, int E, int k, int S, float coef, int32_t* counts, float* mean_prob,
+                                int32_t* tokens, float* loss, void* ws, cudaStream_t st);
+cudaError_t launch_route_backward(const float* logits, const int32_t* idx, const float* gates, const float* dgates,
+                                  const float* dloss, const int32_t* counts, const int32_t* tokens,
+                                  const int32_t* seq_off, const uint8_t* mask, int T, int E, int k, int S, float coef,
+                                  float* dlogits, int32_t* flag, cudaStream_t st);
+
+// ---- 8-bit activation checkpoints (ckpt.cu) and the products that read them (grad_gemm.cu) ----
+cudaError_t launch_ckpt_pack(const void* x, long long ldx, int T, int K, uint8_t* codes, uint8_t* scales,
+                             cudaStream_t st);
+cudaError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int T, int K, void* x, long long ldx,
+                               cudaStream_t st);
+cudaError_t launch_ckpt_swiglu_backward(const uint8_t* codes, const uint8_t* scales, const void* dh, long long lddh,
+                                        int T, int I, void* dgu, void* h, cudaStream_t st);
+size_t wgrad_workspace_bytes(int R, int N, int K, int G);
+cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* codes, const uint8_t* scales,
+                              const int32_t* offsets, const int32_t* perm, int k, int R, int rows, int N, int K, int G,
+                              float* dw, int accumulate, void* ws, uint64_t wait_ns, cudaStream_t st);
+size_t router_backward_workspace_bytes(int T, int H, int E);
+cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t* codes, const uint8_t* scales,
+                                   const float* w, int T, int H, int E, void* dx, float* dw, float* db, int accumulate,
+                                   void* ws, uint64_t wait_ns, cudaStream_t st);
+
 }  // namespace moe

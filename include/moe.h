@@ -310,6 +310,133 @@ size_t moe_fp8_workspace_bytes(int T_max, int N, int K);
 int moe_fp8_linear(const void *x_bf16, int T, int N, int K, const void *packed, void *y_bf16, void *ws,
                    size_t ws_bytes, uint8_t *dbg_q, uint8_t *dbg_s, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Training the router and the projections around the experts.  The pages name
+ * no training; these calls use the usual definitions and this library's own
+ * routing (moe_route), sort (moe_sort) and FP8 block format (moe_fp8_linear).
+ * All are asynchronous and graph-capturable, and their results do not depend
+ * on the order in which thread blocks run.  A workspace (and its error word)
+ * belongs to one call at a time: calls and replayed graphs that may overlap
+ * need one each.
+ * ------------------------------------------------------------------------- */
+
+/* Load-balance loss and per-expert counts of routed tokens.
+ * The rows of logits [T, E] fp32 and topk_idx [T, k] int32 (as moe_route reads
+ * and writes them) fall into S sequences: sequence s holds the rows
+ * seq_offsets[s] <= t < seq_offsets[s + 1] (ascending, within [0, T]; rows in
+ * front of the first or behind the last sequence are padding).  seq_offsets
+ * NULL: one sequence of all T rows (S = 1).  token_mask [T] uint8 (or NULL)
+ * takes out the rows where it is 0.  With V_s the rows left to sequence s,
+ * n_s their number and S' the number of sequences with n_s > 0:
+ *   counts[s, e] = |{(t, j): t in V_s, topk_idx[t, j] = e}|          [S, E] int32
+ *   mean_prob[s, e] = (1 / n_s) sum_{t in V_s} softmax(logits[t])_e  [S, E] fp32, or NULL
+ *   loss = coef / S' * sum_s sum_e (E counts[s, e] / (k n_s)) mean_prob[s, e]   [1] fp32
+ *   tokens [S + 1] int32: n_s, and S' at the end.
+ * Sequences without rows have counts and mean_prob 0 and add nothing; the loss
+ * of no rows is 0.  A row whose logits are all -inf has probabilities 0; a NaN
+ * or +inf logit makes its row NaN.  Sums are fp32 (the loss's last one fp64).
+ * The loss is coef for a perfectly balanced router.
+ * ws: moe_balance_workspace_bytes(T_max, E, S_max) bytes, 256-byte aligned,
+ * T <= T_max, S <= S_max; its first int32 is the device error word, cleared by
+ * this call: MOE_FLAG_BAD_EXPERT for an id outside [0, E) (left out of the
+ * counts), MOE_FLAG_BOUNDS for offsets that do not ascend within [0, T].
+ * 1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 65535. */
+size_t moe_balance_workspace_bytes(int T_max, int E, int S_max);
+int moe_balance_loss(const float *logits, const int32_t *topk_idx, const int32_t *seq_offsets,
+                     const uint8_t *token_mask, int T, int E, int k, int S, float coef, int32_t *counts,
+                     float *mean_prob, int32_t *tokens, float *loss, void *ws, size_t ws_bytes,
+                     cudaStream_t stream);
+
+/* Gradient of the logits from the balance loss and from the gates.
+ *   dlogits[t, e] = dloss coef / (S' n_s) p_te (f_se - sum_e' p_te' f_se')       (t in V_s)
+ *                 + sum_{j: topk_idx[t, j] = e} gates[t, j] (dgates[t, j] - sum_j' gates[t, j'] dgates[t, j'])
+ * with p_t = softmax(logits[t]), f_se = E counts[s, e] / (k n_s), and counts,
+ * tokens, seq_offsets, token_mask, S and coef as moe_balance_loss took and gave
+ * them (the counts are constants of the gradient).  dloss [1] fp32 device
+ * pointer, or NULL for no balance term (counts, tokens are not read);
+ * dgates [T, k] fp32, or NULL for no gates' term (gates is not read); not both
+ * NULL.  The gates' term covers every row, masked or not.  An expert chosen
+ * twice by a row receives both terms.  dlogits [T, E] is written whole, and
+ * must not overlap logits.  An id outside [0, E) is left out and, when flag
+ * (one int32 device word, or a workspace, or NULL) is given, raises
+ * MOE_FLAG_BAD_EXPERT there: the call adds bits to that word, it clears none. */
+int moe_route_backward(const float *logits, const int32_t *topk_idx, const float *gates, const float *dgates,
+                       const float *dloss, const int32_t *counts, const int32_t *tokens,
+                       const int32_t *seq_offsets, const uint8_t *token_mask, int T, int E, int k, int S,
+                       float coef, float *dlogits, int32_t *flag, cudaStream_t stream);
+
+/* Gradients of moe_router_logits:
+ *   dx[t, h] = bf16( sum_e dlogits[t, e] w_router[e, h] )   [T, H] bf16, or NULL
+ *   dw[e, h] = sum_t dlogits[t, e] x[t, h]                  [E, H] fp32, or NULL
+ *   dbias[e] = sum_t dlogits[t, e]                          [E] fp32, or NULL
+ * at least one of them.  x comes either as x_bf16 [T, H] or as an 8-bit
+ * checkpoint (x_codes, x_scales, see moe_ckpt_pack; H % 128 == 0), the other
+ * being NULL; neither is needed when dw is NULL.  w_router is needed for dx.
+ * accumulate 1 adds dw and dbias to what is there (dx is always overwritten).
+ * Products of fp32 operands are formed from exact bf16 parts, accumulated in
+ * fp32: dw from all three parts of dlogits, dx from the leading two parts of
+ * each operand (about 16 bits, before its rounding to 8).
+ * ws: moe_router_backward_workspace_bytes(T_max, H, E) bytes, 256-byte
+ * aligned, T <= T_max; first int32: the error word, cleared by this call
+ * (MOE_FLAG_TIMEOUT as in moe_forward).  H % 32 == 0, 1 <= E <= 1024; dlogits,
+ * x_bf16, x_codes, w_router, dx, dw 16-byte aligned.  T == 0 leaves dw and
+ * dbias 0 (accumulate 1: unchanged). */
+size_t moe_router_backward_workspace_bytes(int T_max, int H, int E);
+int moe_router_logits_backward(const float *dlogits, const void *x_bf16, const uint8_t *x_codes,
+                               const uint8_t *x_scales, const float *w_router, int T, int H, int E,
+                               void *dx_bf16, float *dw, float *dbias, int accumulate, void *ws,
+                               size_t ws_bytes, cudaStream_t stream);
+
+/* 8-bit activation checkpoints: x [T, K] bf16, row stride ldx >= K elements
+ * (ldx % 8 == 0, x 16-byte aligned), kept as E4M3 codes [T, K] and UE8M0 bytes
+ * scales [T, K/128] and restored as bf16( code * 2^(byte - 127) ).  The rule is
+ * moe_fp8_linear's for its input (whose dbg_q and dbg_s are a checkpoint of
+ * x): per row and 128-input block the smallest power of two 2^e with
+ * max|x| <= 448 * 2^e, byte e + 127, codes rounded to nearest even.  The
+ * maximum is taken over finite values; a NaN or infinity is kept as the NaN
+ * code 0x7F and restored as NaN; magnitudes above 240 * 2^120 (with e = 120)
+ * are kept as that value.  K % 128 == 0; codes and scales contiguous, codes
+ * 16-byte aligned.  In a call that reads a checkpoint a scale byte 0xFF makes
+ * its block NaN. */
+int moe_ckpt_pack(const void *x_bf16, int64_t ldx, int T, int K, uint8_t *codes, uint8_t *scales,
+                  cudaStream_t stream);
+int moe_ckpt_unpack(const uint8_t *codes, const uint8_t *scales, int T, int K, void *x_bf16, int64_t ldx,
+                    cudaStream_t stream);
+
+/* Gradient of SwiGLU from an 8-bit checkpoint of its inputs.  gu_codes
+ * [T, 2I], gu_scales [T, 2I/128]: columns [0, I) gate g, [I, 2I) up u (the row
+ * order of W1); dh [T, I] bf16 with row stride lddh >= I (lddh % 8 == 0).  With
+ * s = 1 / (1 + exp(-g)):
+ *   dgu [T, 2I] bf16: dg = dh u s (1 + g (1 - s)), du = dh g s
+ *   h   [T, I] bf16 (or NULL): g s u, the activation again for the weight
+ *       gradient of the projection behind it
+ * fp32, one rounding per output.  I % 128 == 0; all but scales 16-byte aligned. */
+int moe_ckpt_swiglu_backward(const uint8_t *gu_codes, const uint8_t *gu_scales, const void *dh_bf16,
+                             int64_t lddh, int T, int I, void *dgu_bf16, void *h_bf16, cudaStream_t stream);
+
+/* Weight gradient of a projection y = x W^T from an 8-bit checkpoint of x.
+ * dy [R, N] bf16 with row stride lddy >= N (lddy % 8 == 0); x_codes [X, K],
+ * x_scales [X, K/128].  G groups of rows, group g the rows
+ * offsets[g] <= i < offsets[g + 1] (offsets [G + 1] int32 on the device, as
+ * moe_sort writes them; NULL: G = 1, all R rows):
+ *   dw[g, n, k] = sum_{i in group g} dy[i, n] x^[row(i), k]      [G, N, K] fp32
+ * with x^ the restored checkpoint and row(i) = i, or perm[i] / k_div when perm
+ * [R] is given: with moe_sort's perm and k_div = k, dy in sorted order meets
+ * the tokens' x in token order (W1); without it both are in sorted order (W2).
+ * A group without rows gives 0.  Rows outside every group are not read.
+ * accumulate 1 adds to what dw holds.  bf16 x bf16 products on the tensor
+ * cores (x^ as bf16 is exact), fp32 accumulation.
+ * ws: moe_ckpt_wgrad_workspace_bytes(R_max, N, K, G) bytes, 256-byte aligned,
+ * R <= R_max; its first int32 is the error word, cleared by this call:
+ * MOE_FLAG_BOUNDS for offsets that do not ascend within [0, R] or a row
+ * outside [0, X) (row 0 is used), MOE_FLAG_TIMEOUT as in moe_forward.
+ * N % 8 == 0, K % 128 == 0, 1 <= G <= 1024, without perm X >= R;
+ * dy, x_codes, dw 16-byte aligned. */
+size_t moe_ckpt_wgrad_workspace_bytes(int R_max, int N, int K, int G);
+int moe_ckpt_wgrad(const void *dy_bf16, int64_t lddy, const uint8_t *x_codes, const uint8_t *x_scales,
+                   const int32_t *offsets, const int32_t *perm, int k_div, int R, int X, int N, int K, int G,
+                   float *dw, int accumulate, void *ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Process-wide options.  Each call reads them once when it starts, so a call
  * sees one consistent set; a change made while calls are being enqueued on
  * other host threads applies from the next call that starts after it.
