@@ -1,90 +1,744 @@
-// Gradient products: the weight gradient of a projection from an 8-bit
-// checkpoint of its input (dense, or one per expert), and the gradients of the
-// router projection.  Formulas at moe_ckpt_wgrad and
-// moe_router_logits_backward in the header.
+// Gradient products on the tensor cores: the weight gradient of a projection
+// from an 8-bit checkpoint of its input (dense, or one per expert), and the
+// gradients of the router projection.  Formulas at moe_ckpt_wgrad and
+// moe_router_logits_backward in the header.  All are
+//   C[m, n] = sum_r A[r, m] B[r, n]
+// with bf16 operands and fp32 accumulation (tcgen05 kind::f16):
+//   GM_WGRAD   r = rows, A = dy (bf16), B = the checkpoint's values, which are
+//              exact in bf16 (4 significant bits times a power of two)
+//   GM_RDW     r = tokens, A = dlogits, B = x (bf16 or a checkpoint); dlogits
+//              is fp32 and enters as three bf16 parts of 8 bits each (exact):
+//              three products
+//   GM_RDX     r = experts, A = dlogits, B = w_router, both fp32 with a bf16
+//              result: the leading two parts of each, three products (the
+//              smallest, low x low, is below 2^-16 of the terms)
+// k_router_split writes the fp32 operands' parts to the workspace first.
 //
-// All are C[m, n] = sum_r A[r, m] B[r, n] over rows r.  This form runs on the
-// CUDA cores: 64 x 64 outputs per CTA, 16 rows per step, fp32 fused
-// multiply-adds in ascending r.
+// One SM pair (cluster of two CTAs, tcgen05 cta_group::2) per 256 x 256 tile of
+// C: the CTA of rank q supplies columns 128 q .. + 127 of A's and of B's tile
+// and holds rows 128 q .. + 127 of the accumulator.  A stage is 64 rows r.
+//   warp 0        bf16 operands by TMA (128-byte swizzle; "MN-major", the
+//                 contraction runs over smem rows, except A of GM_RDX)
+//   warp 1        (leader CTA) issues the MMAs
+//   warps 2, 3    checkpoint: codes by cp.async (rows through perm), scales
+//   warps 4-7     checkpoint: codes to bf16, into the swizzled stage.  Without
+//                 one, warp 4 passes "landed" on to the leader
+//   warps 8-15    epilogue, from two 256-column accumulators in TMEM
+// Work: pair p takes the tiles p, p + P, ... of the first floor(tiles / P) P
+// ones whole; the remaining tiles are cut into chunks of rows and dealt out
+// evenly, so that the last round is not left to a few pairs.  Parts of a tile
+// go to the workspace and k_grad_fixup adds them in a fixed order.
+//
+// The tensor cores truncate when they add to the fp32 accumulator, always
+// towards zero: about 7e-9 of the result per MMA (measured: 1.2e-6 after 256
+// of them, against 6e-7 of an fp32 sum in CUDA cores).  So an accumulator is
+// drained every ACC_STEPS stages and added up in the epilogue's registers,
+// rounding to nearest.
 #include "ckpt.cuh"
 #include "kernels.cuh"
 #include "moe_common.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 
-constexpr int kGradT = 64, kGradK = 16;
+enum { GM_WGRAD = 0, GM_RDW = 1, GM_RDX = 2 };
 
-struct Bf16Rows {          // v[r, c] of a bf16 matrix
-    const __nv_bfloat16* p;
-    long long ld;
-    __device__ float operator()(int r, int c) const { return __bfloat162float(p[r * ld + c]); }
+constexpr int GG_TILE = 256;            // rows and columns of C per pair
+constexpr int GG_HALF = 128;            // per CTA: rows of A's tile, columns of B's
+constexpr int GG_K = 64;                // contraction rows per stage
+constexpr int GG_PLANE = GG_HALF * GG_K * 2;   // one operand part of a stage, per CTA
+constexpr int GG_BLOCK = GG_K * 128;    // 64 columns of an MN-major plane
+constexpr int GG_CONV_WARP0 = 4, GG_CONV_WARPS = 4, GG_EPI_WARP0 = 8, GG_EPI_WARPS = 8;
+constexpr int GG_THREADS = 32 * (GG_EPI_WARP0 + GG_EPI_WARPS);
+constexpr int GG_MAX_PAIRS = 128;
+// Registers per thread: at launch, and of the three kinds of warpgroup after
+// setmaxnreg.  The epilogue holds 128 sums per thread.
+constexpr int GG_REGS = 128, GG_REGS_LOAD = 72, GG_REGS_CONV = 104, GG_REGS_EPI = 168;
+static_assert(GG_REGS_LOAD + GG_REGS_CONV + 2 * GG_REGS_EPI <= 4 * GG_REGS, "registers of the block");
+
+template <int MODE, bool CK>
+struct GradCfg {
+    static constexpr int AP = MODE == GM_WGRAD ? 1 : MODE == GM_RDW ? 3 : 2;   // parts of A
+    static constexpr int BP = MODE == GM_RDX ? 2 : 1;
+    static constexpr int OPS = (AP + BP) * GG_PLANE;
+    static constexpr int RAW = CK ? GG_K * GG_HALF + GG_K * 4 : 0;             // codes, scales (bf16 pairs)
+    static constexpr int STAGES = MODE == GM_WGRAD ? 5 : 3;
+    static constexpr int ACC_STEPS = MODE == GM_WGRAD ? 8 : MODE == GM_RDW ? 4 : 16;
+    // rows per chunk of a split tile (a result of GM_RDX has at most 16 stages and is not split)
+    static constexpr int CHUNK_STEPS = MODE == GM_WGRAD ? 16 : MODE == GM_RDW ? 8 : 16;
 };
-struct F32Rows {
-    const float* p;
-    long long ld;
-    __device__ float operator()(int r, int c) const { return p[r * ld + c]; }
+
+template <int MODE, bool CK>
+struct GradShared {
+    uint8_t ops[GradCfg<MODE, CK>::STAGES][GradCfg<MODE, CK>::OPS];      // 1024-byte aligned
+    uint8_t raw[GradCfg<MODE, CK>::STAGES][CK ? GradCfg<MODE, CK>::RAW : 16];
+    uint64_t landed[GradCfg<MODE, CK>::STAGES];      // TMA bytes of this CTA
+    uint64_t raw_full[GradCfg<MODE, CK>::STAGES], raw_empty[GradCfg<MODE, CK>::STAGES];
+    uint64_t ready[GradCfg<MODE, CK>::STAGES];       // leader: both CTAs' operands are in place
+    uint64_t empty[GradCfg<MODE, CK>::STAGES];
+    uint64_t acc_full[2], acc_empty[2], drain;
+    uint32_t tmem_base;
+    int32_t abort;
+    int32_t rem_pre[GG_MAX_PAIRS + 1];               // chunks in front of each split tile
 };
-struct F32Cols {           // the transpose of a row-major matrix
-    const float* p;
-    long long ld;
-    __device__ float operator()(int r, int c) const { return p[c * ld + r]; }
-};
-struct CkptRows {          // a checkpoint's rows, through perm[r] / k when given
-    const uint8_t* codes;
+
+struct GradArgs {
+    const uint8_t* codes;      // checkpoint of B, or NULL
     const uint8_t* scales;
+    const int32_t* offsets;    // groups of rows, or NULL
     const int32_t* perm;
-    int k, rows, K;
-    int32_t* flag;
-    __device__ float operator()(int r, int c) const {
-        const int t = perm ? checked_index(perm[r] / k, rows, flag) : r;
-        return e4m3x2_value(codes[(size_t)t * K + c]).x * ckpt_scale(scales[(size_t)t * (K / 128) + c / 128]);
-    }
-};
-struct StoreF32 {
-    float* p;
-    long long ld, group;
+    int k_div, xrows;          // checkpoint row = perm[i] / k_div, below xrows
+    int R;                     // contraction rows of all groups
+    int M, N, G;               // C is [G, M, N]
+    int MT, NT, tiles, full, chunk_steps;
+    float* c;
+    __nv_bfloat16* cb;         // GM_RDX
     int accumulate;
-    __device__ void operator()(int g, int m, int n, float v) const {
-        float* d = p + g * group + m * ld + n;
-        *d = accumulate ? *d + v : v;
-    }
-};
-struct StoreBf16 {
-    __nv_bfloat16* p;
-    long long ld;
-    __device__ void operator()(int, int m, int n, float v) const { p[m * ld + n] = __float2bfloat16_rn(v); }
+    float* part;               // [pairs][2][256][256]
+    int32_t* flag;
+    uint64_t wait_ns;
 };
 
-template <class A, class B, class C>
-__global__ void __launch_bounds__(256) k_grad_simt(A a, B b, C c, const int32_t* offsets, int R, int M, int N) {
-    pdl_begin();
-    __shared__ float as[kGradK][kGradT + 4], bs[kGradK][kGradT + 4];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int n0 = blockIdx.x * kGradT, m0 = blockIdx.y * kGradT, g = blockIdx.z;
-    const int r0 = offsets ? min(max(offsets[g], 0), R) : 0;
-    const int r1 = offsets ? min(max(offsets[g + 1], 0), R) : R;
-    float acc[4][4] = {};
-    for (int r = r0; r < r1; r += kGradK) {
-        for (int i = tid; i < kGradK * kGradT; i += 256) {
-            const int rr = i / kGradT, cc = i % kGradT;
-            as[rr][cc] = (r + rr < r1 && m0 + cc < M) ? a(r + rr, m0 + cc) : 0.0f;
-            bs[rr][cc] = (r + rr < r1 && n0 + cc < N) ? b(r + rr, n0 + cc) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < kGradK; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = fmaf(as[kk][ty + 16 * i], bs[kk][tx + 16 * j], acc[i][j]);
-        __syncthreads();
+// ---- PTX forms of the SM pair ----------------------------------------------------
+__device__ __forceinline__ uint32_t gg_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void gg_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t gg_peer(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void gg_arrive(uint32_t bar, uint32_t rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(gg_peer(bar, rank)) : "memory");
+}
+__device__ __forceinline__ void gg_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void gg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void gg_tma(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void gg_cp16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+template <int REGS>
+__device__ __forceinline__ void gg_regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void gg_regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+__device__ __forceinline__ void gg_fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void gg_st16(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+// 16 lanes x 32 columns: lane t holds, for j = 0..3, r[4j], r[4j+1] = row t/4,
+// columns 8j + 2(t%4) + {0, 1}, and r[4j+2], r[4j+3] = row 8 + t/4.
+__device__ __forceinline__ void gg_ld16x32(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Shared-memory descriptors, 128-byte swizzle (type 2 in bits 61-63).
+// MN-major (contraction over smem rows of 128 bytes = 64 columns): 8-row groups
+// 1 KB apart, the next 64 columns 8 KB apart.  K-major (128-byte rows are 64
+// contraction values of one row of C): 8-row groups 1 KB apart.
+__device__ __forceinline__ uint64_t gg_desc_mn(uint32_t addr) {
+    return make_sdesc(addr, GG_BLOCK, 1024) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t gg_desc_k(uint32_t addr) { return make_sdesc(addr, 16, 1024) | ((uint64_t)2 << 61); }
+
+// kind::f16 instruction descriptor: bf16 x bf16, fp32 accumulate, M = N = 256.
+__device__ __forceinline__ uint32_t gg_idesc(bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(GG_TILE >> 3) << 17) | ((uint32_t)(GG_TILE >> 4) << 24);
+}
+
+// Address of 16-byte chunk c (0..7) of row r of a 128-byte-row block, swizzled.
+__device__ __forceinline__ uint32_t gg_swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// ---- the split of the work --------------------------------------------------------
+// Contraction rows [r0, r1) of a group.
+__device__ __forceinline__ void gg_rows(const GradArgs& a, int g, int& r0, int& r1) {
+    r0 = 0;
+    r1 = a.R;
+    if (a.offsets) {
+        r0 = min(max(__ldg(a.offsets + g), 0), a.R);
+        r1 = min(max(__ldg(a.offsets + g + 1), r0), a.R);
     }
+}
+// (a group without rows still has one stage, of zeros)
+__device__ __forceinline__ int gg_steps(int rows) { return max(1, (int)(((long long)rows + GG_K - 1) / GG_K)); }
+
+struct Segment {
+    int m0, n0, g;      // tile
+    int r0, r1;         // contraction rows of its group
+    int s0, s1;         // stages
+    int slot;           // -1: the whole tile, else the part's place
+};
+
+// Walks a pair's segments; every role walks the same ones.
+struct Walk {
+    const GradArgs* args;
+    const int32_t* rem_pre;
+    int pair, pairs, next_full, chunk, chunk_end;
+    bool first_part;
+    __device__ Walk(const GradArgs& a, const int32_t* pre, int p, int P)
+        : args(&a), rem_pre(pre), pair(p), pairs(P), next_full(p), first_part(true) {
+        const int rem = a.tiles - a.full;
+        const long long W = rem > 0 ? pre[rem] : 0;
+        chunk = (int)(W * p / P);
+        chunk_end = (int)(W * (p + 1) / P);
+    }
+    __device__ bool next(Segment& s) {
+        const GradArgs& a = *args;
+        int t;
+        if (next_full < a.full) {
+            t = next_full;
+            next_full += pairs;
+        } else if (chunk < chunk_end) {
+            int lo = 0, hi = a.tiles - a.full - 1;        // last tile with rem_pre <= chunk
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (rem_pre[mid] <= chunk) lo = mid; else hi = mid - 1;
+            }
+            t = a.full + lo;
+        } else {
+            return false;
+        }
+        const int per = a.MT * a.NT, i = t % per;
+        s.g = t / per;
+        s.m0 = (i / a.NT) * GG_TILE;
+        s.n0 = (i % a.NT) * GG_TILE;
+        gg_rows(a, s.g, s.r0, s.r1);
+        const int steps = gg_steps(s.r1 - s.r0);
+        s.s0 = 0;
+        s.s1 = steps;
+        s.slot = -1;
+        if (t >= a.full) {
+            const int b = rem_pre[t - a.full], e = rem_pre[t - a.full + 1];
+            const int c1 = min(chunk_end, e);
+            if (chunk > b || c1 < e) {
+                s.slot = pair * 2 + (first_part ? 0 : 1);
+                s.s0 = (chunk - b) * a.chunk_steps;
+                s.s1 = min(steps, (c1 - b) * a.chunk_steps);
+            }
+            first_part = false;
+            chunk = c1;
+        }
+        return true;
+    }
+};
+
+// The stages of a pair's segments one by one.
+struct Steps {
+    Walk walk;
+    Segment seg;
+    int st;
+    bool on;
+    __device__ Steps(const Walk& w) : walk(w) {
+        on = walk.next(seg);
+        st = on ? seg.s0 : 0;
+    }
+    __device__ void advance() {
+        if (on && ++st == seg.s1) {
+            on = walk.next(seg);
+            st = seg.s0;
+        }
+    }
+};
+
+// ---- the kernel ----------------------------------------------------------------------
+template <int MODE, bool CK>
+__global__ void __launch_bounds__(GG_THREADS, 1)
+    k_grad_gemm(const __grid_constant__ GradArgs a, const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map) {
+    pdl_begin();
+    using Cfg = GradCfg<MODE, CK>;
+    constexpr int AP = Cfg::AP, BP = Cfg::BP, STAGES = Cfg::STAGES;
+    extern __shared__ uint8_t gg_raw_smem[];
+    GradShared<MODE, CK>& sh =
+        *reinterpret_cast<GradShared<MODE, CK>*>(gg_raw_smem + ((1024u - (smem_u32(gg_raw_smem) & 1023u)) & 1023u));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = gg_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&sh.landed[s]), 1);
+            mbar_init(smem_u32(&sh.raw_full[s]), 128);      // two warps, a copy's and a plain arrival per lane
+            mbar_init(smem_u32(&sh.raw_empty[s]), GG_CONV_WARPS);
+            mbar_init(smem_u32(&sh.ready[s]), 2 * (CK ? GG_CONV_WARPS : 1));
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&sh.acc_full[b]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[b]), 2 * GG_EPI_WARPS);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) {
+        // chunks in front of each split tile (fewer than `pairs` tiles)
+        const int rem = a.tiles - a.full;
+        int run = 0;
+        for (int i0 = 0; i0 < rem; i0 += 32) {
+            int n = 0;
+            if (i0 + lane < rem) {
+                int r0, r1;
+                gg_rows(a, (a.full + i0 + lane) / (a.MT * a.NT), r0, r1);
+                n = (gg_steps(r1 - r0) + a.chunk_steps - 1) / a.chunk_steps;
+            }
+            int x = n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (i0 + lane < rem) sh.rem_pre[i0 + lane] = run + x - n;
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) sh.rem_pre[rem] = run;
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    gg_cluster_sync();      // the peer's barriers exist before any remote arrive
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    volatile int32_t* abort = &sh.abort;
+    auto give_up = [&]() {
+        *abort = 1;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(gg_peer(smem_u32(&sh.abort), rank ^ 1u)), "r"(1u)
+                     : "memory");
+        raise_flag(a.flag, FLAG_TIMEOUT);
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_for<true>(bar, parity, a.wait_ns, abort); };
+    // of a whole warp: its lanes go on or give up together
+    auto warp_wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, !*abort && wait(bar, parity)) != 0;
+    };
+    auto final_wait = [&](uint32_t bar, uint32_t parity) {
+        if (!mbar_wait_for<true>(bar, parity, a.wait_ns, nullptr)) raise_flag(a.flag, FLAG_TIMEOUT);
+    };
+    const Walk walk0(a, sh.rem_pre, pair, pairs);
+    int stage = 0;
+    uint32_t phase = 0;
+    auto next_stage = [&]() {
+        if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    };
+
+    if (warp < GG_CONV_WARP0) {
+        gg_regs_down<GG_REGS_LOAD>();
+        if (warp == 0 && lane == 0) {
+            // ---------------- bf16 operands by TMA ----------------
+            uint32_t filled = 0, parity = 0;      // bit s: stage s has a copy, and its phase
+            constexpr uint32_t bytes = (AP + (CK ? 0 : BP)) * GG_PLANE;
+            for (Steps s(walk0); s.on; s.advance()) {
+                if (*abort || !wait(smem_u32(&sh.empty[stage]), phase ^ 1u)) {
+                    give_up();
+                    break;
+                }
+                const uint32_t bar = smem_u32(&sh.landed[stage]);
+                uint32_t dst = smem_u32(sh.ops[stage]);
+                const int r = s.seg.r0 + s.st * GG_K;
+                const int m = s.seg.m0 + GG_HALF * (int)rank, n = s.seg.n0 + GG_HALF * (int)rank;
+                mbar_expect_tx(bar, bytes);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (m0 + ty + 16 * i < M && n0 + tx + 16 * j < N) c(g, m0 + ty + 16 * i, n0 + tx + 16 * j, acc[i][j]);
+                for (int p = 0; p < AP; ++p, dst += GG_PLANE) {
+                    if (MODE == GM_RDX) {
+                        gg_tma(dst, &a_map, r, m, p, bar);
+                    } else {
+                        gg_tma(dst, &a_map, m, r, p, bar);
+                        gg_tma(dst + GG_BLOCK, &a_map, m + 64, r, p, bar);
+                    }
+                }
+                if (!CK) {
+#pragma unroll
+                    for (int p = 0; p < BP; ++p, dst += GG_PLANE) {
+                        gg_tma(dst, &b_map, n, r, p, bar);
+                        gg_tma(dst + GG_BLOCK, &b_map, n + 64, r, p, bar);
+                    }
+                }
+                filled |= 1u << stage;
+                parity = (parity & ~(1u << stage)) | (phase << stage);
+                next_stage();
+            }
+            for (int s = 0; s < STAGES; ++s)
+                if (filled >> s & 1u) final_wait(smem_u32(&sh.landed[s]), parity >> s & 1u);
+        } else if (warp == 1 && lane == 0) {
+            // ---------------- MMA issuer ----------------
+            if (rank == 0) {
+                int buf = 0;
+                uint32_t use = 0;       // bit b: parity of accumulator b's next use
+                const uint32_t idesc = gg_idesc(MODE != GM_RDX, true);
+                Walk walk(walk0);
+                Segment seg;
+                bool ok = true;
+                while (ok && walk.next(seg)) {
+                    for (int st = seg.s0; ok && st < seg.s1;) {
+                        const int st1 = min(seg.s1, st + Cfg::ACC_STEPS);
+                        if (!wait(smem_u32(&sh.acc_empty[buf]), (use >> buf & 1u) ^ 1u)) {
+                            give_up();
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t d = tmem + buf * GG_TILE;
+                        for (int s = st; s < st1; ++s) {
+                            if (!wait(smem_u32(&sh.ready[stage]), phase)) {
+                                give_up();
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t sa = smem_u32(sh.ops[stage]), sb = sa + AP * GG_PLANE;
+                            auto product = [&](int pa, int pb, bool first) {
+#pragma unroll
+                                for (int kk = 0; kk < GG_K / 16; ++kk) {
+                                    const uint64_t da = MODE == GM_RDX ? gg_desc_k(sa + pa * GG_PLANE + kk * 32)
+                                                                       : gg_desc_mn(sa + pa * GG_PLANE + kk * 2048);
+                                    gg_mma(d, da, gg_desc_mn(sb + pb * GG_PLANE + kk * 2048), idesc,
+                                           !(first && s == st && kk == 0));
+                                }
+                            };
+                            if constexpr (MODE == GM_WGRAD) {
+                                product(0, 0, true);
+                            } else if constexpr (MODE == GM_RDW) {
+                                product(2, 0, true);
+                                product(1, 0, false);
+                                product(0, 0, false);
+                            } else {
+                                product(1, 0, true);
+                                product(0, 1, false);
+                                product(0, 0, false);
+                            }
+                            gg_commit(smem_u32(&sh.empty[stage]));
+                            next_stage();
+                        }
+                        if (!ok) break;
+                        gg_commit(smem_u32(&sh.acc_full[buf]));
+                        use ^= 1u << buf;
+                        buf ^= 1;
+                        st = st1;
+                    }
+                }
+                gg_commit(smem_u32(&sh.drain));
+            }
+            // every MMA is done before either CTA frees its TMEM
+            final_wait(smem_u32(&sh.drain), 0);
+        } else if (CK && warp >= 2) {
+            // ---------------- checkpoint codes and scales ----------------
+            // Lane = row of this warp's 32; row indices are resolved two stages
+            // ahead and scale bytes read one stage ahead of the copies.
+            const int half = 32 * (warp - 2);
+            auto read_perm = [&](const Steps& s) {
+                const int i = s.seg.r0 + s.st * GG_K + half + lane;
+                if (!s.on || i >= s.seg.r1 || s.seg.n0 + GG_HALF * (int)rank >= a.N) return -1;
+                return a.perm ? __ldg(a.perm + i) : i;
+            };
+            // the checkpoint row of a table entry (-1: a row of zeros)
+            auto resolve = [&](const Steps& s, int v) {
+                const int i = s.seg.r0 + s.st * GG_K + half + lane;
+                if (!s.on || i >= s.seg.r1 || s.seg.n0 + GG_HALF * (int)rank >= a.N) return -1;
+                return a.perm ? checked_index(v < 0 ? v : v / a.k_div, a.xrows, a.flag) : v;
+            };
+            auto read_scale = [&](const Steps& s, int x) -> uint32_t {
+                if (x < 0) return 0u;
+                return __ldg(a.scales + (size_t)x * (a.N >> 7) + ((s.seg.n0 >> 7) + rank));
+            };
+            Steps s0(walk0);
+            Steps s2(s0);
+            int x0 = resolve(s0, read_perm(s0));
+            uint32_t b0 = read_scale(s0, x0);
+            s2.advance();
+            Steps s1(s2);
+            int v1 = read_perm(s1);
+            for (; s0.on;) {
+                s2.advance();
+                const int x1 = resolve(s1, v1);
+                const uint32_t b1 = read_scale(s1, x1);
+                const int v2 = read_perm(s2);
+                if (!warp_wait(smem_u32(&sh.raw_empty[stage]), phase ^ 1u)) {
+                    give_up();
+                    break;
+                }
+                const uint32_t raw = smem_u32(sh.raw[stage]), bar = smem_u32(&sh.raw_full[stage]);
+                {
+                    // 2^(byte - 127) as a pair of bf16 (exact)
+                    const uint32_t h = __float_as_uint(ckpt_scale(b0)) >> 16;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(raw + GG_K * GG_HALF + 4 * (half + lane)),
+                                 "r"(h | h << 16)
+                                 : "memory");
+                }
+                const int n = s0.seg.n0 + GG_HALF * (int)rank;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int row = 4 * j + (lane >> 3);
+                    const int x = __shfl_sync(0xffffffffu, x0, row);
+                    const uint8_t* p = x >= 0 ? a.codes + (size_t)x * a.N + n + 16 * (lane & 7) : a.codes;
+                    gg_cp16(raw + (half + row) * GG_HALF + 16 * (lane & 7), p, x >= 0);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+                mbar_arrive(bar);
+                next_stage();
+                s0 = s1;
+                s1 = s2;
+                x0 = x1;
+                b0 = b1;
+                v1 = v2;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+        __syncwarp();
+    } else if (warp < GG_EPI_WARP0) {
+        gg_regs_down<GG_REGS_CONV>();
+        if (CK) {
+            // ---------------- checkpoint codes to bf16 ----------------
+            // Thread t: 8 codes (8-byte column t % 16) of the rows t / 16 + 8 u.
+            const int t = threadIdx.x - 32 * GG_CONV_WARP0, c = t & 15, rr = t >> 4;
+            const uint32_t doff = (uint32_t)(AP * GG_PLANE + (c >> 3) * GG_BLOCK);
+            for (Steps s(walk0); s.on; s.advance()) {
+                if (!warp_wait(smem_u32(&sh.raw_full[stage]), phase)) {
+                    give_up();
+                    break;
+                }
+                const uint8_t* raw = sh.raw[stage];
+                uint2 q[8];
+                uint32_t f[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    q[u] = *reinterpret_cast<const uint2*>(raw + (rr + 8 * u) * GG_HALF + 8 * c);
+                    f[u] = *reinterpret_cast<const uint32_t*>(raw + GG_K * GG_HALF + 4 * (rr + 8 * u));
+                }
+                if (!warp_wait(smem_u32(&sh.empty[stage]), phase ^ 1u)) {
+                    give_up();
+                    break;
+                }
+                const uint32_t dst = smem_u32(sh.ops[stage]);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    gg_st16(dst + doff + gg_swz(rr + 8 * u, c & 7), ckpt_bf16x8(q[u], f[u]));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[stage]));
+                if (!warp_wait(smem_u32(&sh.landed[stage]), phase)) {
+                    give_up();
+                    break;
+                }
+                if (MODE == GM_WGRAD) {
+                    // rows of the next group in the last stage of this one: dy must not
+                    // meet the zeros of B there (0 x NaN)
+                    const int valid = s.seg.r1 - s.seg.r0 - s.st * GG_K;
+                    if (valid < GG_K)
+                        for (int i = t; i < GG_K * 16; i += 32 * GG_CONV_WARPS)
+                            if ((i >> 3 & (GG_K - 1)) >= valid) gg_st16(dst + i * 16, make_uint4(0u, 0u, 0u, 0u));
+                }
+                gg_fence_async();
+                __syncwarp();
+                if (lane == 0) gg_arrive(smem_u32(&sh.ready[stage]), 0);
+                next_stage();
+            }
+        } else if (warp == GG_CONV_WARP0 && lane == 0) {
+            for (Steps s(walk0); s.on; s.advance()) {
+                if (*abort || !wait(smem_u32(&sh.landed[stage]), phase)) {
+                    give_up();
+                    break;
+                }
+                gg_arrive(smem_u32(&sh.ready[stage]), 0);
+                next_stage();
+            }
+        }
+        __syncwarp();
+    } else {
+        gg_regs_up<GG_REGS_EPI>();
+        // ---------------- epilogue ----------------
+        // Warp (q, half): TMEM lanes 32 q .. + 31, columns 128 half .. + 127.
+        // acc[32 L + 4 jj + 2 hh + e]... see gg_ld16x32: row 32 q + 16 L + 8 hh + t / 4.
+        const int q = warp & 3, half = (warp - GG_EPI_WARP0) >> 2, t4 = lane >> 2, c2 = 2 * (lane & 3);
+        int buf = 0;
+        uint32_t use = 0;
+        Walk walk(walk0);
+        Segment seg;
+        bool ok = true;
+        while (ok && walk.next(seg)) {
+            float acc[2][4][16];       // 16-row half, 32-column group, value
+#pragma unroll
+            for (int i = 0; i < 128; ++i) acc[i >> 6][(i >> 4) & 3][i & 15] = 0.0f;
+            for (int st = seg.s0; st < seg.s1; st += Cfg::ACC_STEPS) {
+                if (!warp_wait(smem_u32(&sh.acc_full[buf]), use >> buf & 1u)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t v[16];
+                    gg_ld16x32(tmem + ((uint32_t)(32 * q + 16 * (i >> 2)) << 16) + buf * GG_TILE + 128 * half + 32 * (i & 3), v);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        acc[i >> 2][i & 3][e] = __fadd_rn(acc[i >> 2][i & 3][e], __uint_as_float(v[e]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) gg_arrive(smem_u32(&sh.acc_empty[buf]), 0);
+                use ^= 1u << buf;
+                buf ^= 1;
+            }
+            if (!ok) break;
+            const bool whole = seg.slot < 0;
+            const int row0 = GG_HALF * (int)rank + 32 * q + t4, col0 = 128 * half;
+            if constexpr (MODE == GM_RDX) {
+                const int mlim = a.M - seg.m0, nlim = a.N - seg.n0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int m = row0 + 8 * k;
+                    __nv_bfloat16* o = a.cb + (size_t)(seg.m0 + m) * a.N + seg.n0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        // 16 columns of a row lie in 4 lanes, 2 in each of two groups of 8:
+                        // exchanged so that a lane stores 4 neighbours
+                        const float* r = &acc[k >> 1][j >> 1][8 * (j & 1) + 2 * (k & 1)];
+                        const uint32_t pe = bf16x2_rn(r[0], r[1]), po = bf16x2_rn(r[4], r[5]);
+                        const int src = (lane & ~3) + 2 * (lane & 1);
+                        const uint32_t e0 = __shfl_sync(0xffffffffu, pe, src), e1 = __shfl_sync(0xffffffffu, pe, src + 1);
+                        const uint32_t o0 = __shfl_sync(0xffffffffu, po, src), o1 = __shfl_sync(0xffffffffu, po, src + 1);
+                        const int col = col0 + 16 * j + 4 * (lane & 3);
+                        if (m < mlim && col < nlim)
+                            *reinterpret_cast<uint2*>(o + col) = (lane & 2) ? make_uint2(o0, o1) : make_uint2(e0, e1);
+                    }
+                }
+            } else {
+                float* out = whole ? a.c + ((size_t)seg.g * a.M + seg.m0) * a.N + seg.n0
+                                   : a.part + (size_t)seg.slot * (GG_TILE * GG_TILE);
+                const size_t ld = whole ? a.N : GG_TILE;
+                const int mlim = whole ? a.M - seg.m0 : GG_TILE, nlim = whole ? a.N - seg.n0 : GG_TILE;
+                const bool add = whole && a.accumulate;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int m = row0 + 8 * k;
+                    if (m >= mlim) continue;
+                    float* o = out + (size_t)m * ld + col0 + c2;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (col0 + 8 * j >= nlim) break;
+                        const float* r = &acc[k >> 1][j >> 2][4 * (j & 3) + 2 * (k & 1)];
+                        float2 w = make_float2(r[0], r[1]);
+                        if (add) {
+                            const float2 b = *reinterpret_cast<const float2*>(o + 8 * j);
+                            w.x = __fadd_rn(b.x, w.x);
+                            w.y = __fadd_rn(b.y, w.y);
+                        }
+                        *reinterpret_cast<float2*>(o + 8 * j) = w;
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    gg_cluster_sync();      // no remote arrive or MMA targets this CTA any more
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// Adds the parts of each split tile in the order of their rows.  CTA (split
+// tile, 8 rows of it).
+__global__ void __launch_bounds__(256) k_grad_fixup(GradArgs a, int pairs) {
+    pdl_begin();
+    const int rem = a.tiles - a.full, i = blockIdx.x;
+    __shared__ int s_b, s_e, s_W;
+    if (threadIdx.x < 32) {
+        // chunks of all split tiles, and of those in front of tile i
+        int all = 0, before = 0, own = 0;
+        for (int j = threadIdx.x; j < rem; j += 32) {
+            int r0, r1;
+            gg_rows(a, (a.full + j) / (a.MT * a.NT), r0, r1);
+            const int n = (gg_steps(r1 - r0) + a.chunk_steps - 1) / a.chunk_steps;
+            all += n;
+            before += j < i ? n : 0;
+            own += j == i ? n : 0;
+        }
+        all = warp_sum(all);
+        before = warp_sum(before);
+        own = warp_sum(own);
+        if (threadIdx.x == 0) {
+            s_W = all;
+            s_b = before;
+            s_e = before + own;
+        }
+    }
+    __syncthreads();
+    const long long W = s_W;
+    auto range0 = [&](int p) { return (int)(W * p / pairs); };
+    // first pair whose range reaches past the tile's first chunk
+    int p0 = (int)((long long)s_b * pairs / W);
+    while (p0 > 0 && range0(p0) > s_b) --p0;
+    while (range0(p0 + 1) <= s_b) ++p0;
+    if (range0(p0 + 1) >= s_e) return;        // one pair computed the whole tile
+    const int per = a.MT * a.NT, t = a.full + i, ti = t % per;
+    const int m0 = (ti / a.NT) * GG_TILE, n0 = (ti % a.NT) * GG_TILE;
+    float* out = a.c + ((size_t)(t / per) * a.M + m0) * a.N + n0;
+    for (int e = threadIdx.x; e < 8 * (GG_TILE / 4); e += 256) {
+        const int m = blockIdx.y * 8 + e / (GG_TILE / 4), n = 4 * (e % (GG_TILE / 4));
+        if (m0 + m >= a.M || n0 + n >= a.N) continue;
+        float4* o = reinterpret_cast<float4*>(out + (size_t)m * a.N + n);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = p0; p < pairs && range0(p) < s_e; ++p) {
+            if (range0(p + 1) == range0(p)) continue;
+            // the tile is the pair's second part when its range begins in an earlier tile
+            const int slot = 2 * p + (range0(p) < s_b ? 1 : 0);
+            const float4 v = __ldg(reinterpret_cast<const float4*>(a.part + (size_t)slot * (GG_TILE * GG_TILE) + m * GG_TILE + n));
+            s.x = __fadd_rn(s.x, v.x);
+            s.y = __fadd_rn(s.y, v.y);
+            s.z = __fadd_rn(s.z, v.z);
+            s.w = __fadd_rn(s.w, v.w);
+        }
+        if (a.accumulate) {
+            const float4 v = *o;
+            s.x = __fadd_rn(v.x, s.x);
+            s.y = __fadd_rn(v.y, s.y);
+            s.z = __fadd_rn(v.z, s.z);
+            s.w = __fadd_rn(v.w, s.w);
+        }
+        *o = s;
+    }
 }
 
 // First kernel of a call: clears the error word, or raises FLAG_BOUNDS there
@@ -99,16 +753,114 @@ __global__ void __launch_bounds__(1024) k_grad_head(const int32_t* offsets, int 
     if (threadIdx.x == 0) *flag = bad ? FLAG_BOUNDS : 0;
 }
 
-// Column sums of dl [T, E]: CTA per 32 columns, warps stride the rows, the
-// warps' sums are added in order.
-__global__ void __launch_bounds__(1024) k_grad_bias(const float* __restrict__ dl, int T, int E, float* db,
-                                                    int accumulate) {
+// ---- the router's fp32 operands as bf16 parts --------------------------------------
+// v = h + m + l, each with 8 significant bits: h and m rounded to nearest, l
+// exact (24 = 8 + 8 + 8 bits).  An infinity or NaN is its own first part.
+__device__ __forceinline__ void split3(float v, float& h, float& m, float& l) {
+    h = __bfloat162float(__float2bfloat16_rn(v));
+    // (a finite value that rounds up to infinity is truncated instead)
+    if (fabsf(h) == INFINITY) h = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+    const float r = h == v ? 0.0f : v - h;
+    m = __bfloat162float(__float2bfloat16_rn(r));
+    l = m == r ? 0.0f : r - m;
+}
+
+constexpr int kSplitThreads = 256;
+constexpr int kSplitMaxCtas = 148 * 4;
+
+struct SplitArgs {
+    const float* dl;         // [T, E]
+    const float* w;          // [E, H] or NULL
+    int T, E, H, Ep;         // Ep: E rounded up to 8
+    int rows;                // tokens per CTA
+    int ctas;                // CTAs of dl; the others take w
+    int parts;               // of dl: 3, 2, or 0 (none written)
+    __nv_bfloat16* dlp;      // [3][T][Ep]
+    __nv_bfloat16* wp;       // [2][E][H]
+    float* bias_part;        // [ctas][E] column sums, or NULL
+    int32_t* flag;
+};
+
+// Thread: 4 neighbouring columns of every (256 / (Ep / 4))-th row of the CTA's.
+// Also clears the call's error word (the first kernel of a call).
+__global__ void __launch_bounds__(kSplitThreads) k_router_split(SplitArgs a) {
+    pdl_begin();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.flag = 0;
+    if ((int)blockIdx.x >= a.ctas) {
+        const size_t n4 = (size_t)a.E * a.H / 4, step = (size_t)(gridDim.x - a.ctas) * kSplitThreads;
+        for (size_t i = (size_t)(blockIdx.x - a.ctas) * kSplitThreads + threadIdx.x; i < n4; i += step) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(a.w) + i);
+            float h[4], m[4], l;
+            split3(v.x, h[0], m[0], l);
+            split3(v.y, h[1], m[1], l);
+            split3(v.z, h[2], m[2], l);
+            split3(v.w, h[3], m[3], l);
+            reinterpret_cast<uint2*>(a.wp)[i] = make_uint2(bf16x2_rn(h[0], h[1]), bf16x2_rn(h[2], h[3]));
+            reinterpret_cast<uint2*>(a.wp)[n4 + i] = make_uint2(bf16x2_rn(m[0], m[1]), bf16x2_rn(m[2], m[3]));
+        }
+        return;
+    }
+    const int c4 = a.Ep / 4, c = 4 * ((int)threadIdx.x % c4), rg = (int)threadIdx.x / c4, rgs = kSplitThreads / c4;
+    const int t0 = blockIdx.x * a.rows, t1 = min(a.T, t0 + a.rows);
+    const bool vec = (a.E & 3) == 0;
+    float sum[4] = {};
+    if (rg < rgs) {
+#pragma unroll 4
+        for (int t = t0 + rg; t < t1; t += rgs) {
+            const float* p = a.dl + (size_t)t * a.E + c;
+            float v[4] = {};
+            if (vec) {
+                if (c < a.E) {
+                    const float4 q = __ldg(reinterpret_cast<const float4*>(p));
+                    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c + j < a.E) v[j] = __ldg(p + j);
+            }
+            float h[4], m[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sum[j] += v[j];
+                split3(v[j], h[j], m[j], l[j]);
+            }
+            if (a.parts) {
+                __nv_bfloat16* o = a.dlp + (size_t)t * a.Ep + c;
+                const size_t plane = (size_t)a.T * a.Ep;
+                *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(h[0], h[1]), bf16x2_rn(h[2], h[3]));
+                *reinterpret_cast<uint2*>(o + plane) = make_uint2(bf16x2_rn(m[0], m[1]), bf16x2_rn(m[2], m[3]));
+                if (a.parts == 3)
+                    *reinterpret_cast<uint2*>(o + 2 * plane) = make_uint2(bf16x2_rn(l[0], l[1]), bf16x2_rn(l[2], l[3]));
+            }
+        }
+    }
+    if (a.bias_part) {
+        // the row groups' sums, added in order
+        __shared__ float s[kSplitThreads][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[threadIdx.x][j] = sum[j];
+        __syncthreads();
+        if (rg == 0) {
+            for (int g = 1; g < rgs; ++g)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] += s[g * c4 + threadIdx.x][j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < a.E) a.bias_part[(size_t)blockIdx.x * a.E + c + j] = sum[j];
+        }
+    }
+}
+
+// dbias: the CTAs' column sums, warps take every 32nd, then in warp order.
+__global__ void __launch_bounds__(1024) k_router_bias(const float* __restrict__ part, int n, int E, float* db,
+                                                      int accumulate) {
     pdl_begin();
     __shared__ float s[32][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
     float v = 0.0f;
     if (e < E)
-        for (int t = warp; t < T; t += 32) v += __ldg(dl + (size_t)t * E + e);
+        for (int i = warp; i < n; i += 32) v += __ldg(part + (size_t)i * E + e);
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && e < E) {
@@ -118,53 +870,227 @@ __global__ void __launch_bounds__(1024) k_grad_bias(const float* __restrict__ dl
     }
 }
 
-size_t wgrad_workspace_bytes(int, int, int, int) { return 256; }
-size_t router_backward_workspace_bytes(int, int, int) { return 256; }
+// ---- host -----------------------------------------------------------------------------
+template <int MODE, bool CK>
+static size_t grad_smem() { return sizeof(GradShared<MODE, CK>) + 1024; }
 
-static dim3 grad_grid(int M, int N, int G) {
-    return dim3((unsigned)((N + kGradT - 1) / kGradT), (unsigned)((M + kGradT - 1) / kGradT), (unsigned)G);
+// CTAs of the kernel that can be resident as pairs (a persistent grid).
+template <int MODE, bool CK>
+static int grad_grid() {
+    static PerContext cache;
+    return cache.get([] {
+        auto kernel = k_grad_gemm<MODE, CK>;
+        const size_t smem = grad_smem<MODE, CK>();
+        int dev = 0, sms = 0, clusters = 0;
+        cudaFuncAttributes fa;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+            cudaFuncGetAttributes(&fa, kernel) != cudaSuccess)
+            return -1;
+        // the warpgroups' register shares are taken from the launch's
+        if (fa.numRegs != GG_REGS) return -1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(sms / 2 * 2);
+        cfg.blockDim = dim3(GG_THREADS);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters <= 0) return -1;
+        return 2 * std::min(clusters, GG_MAX_PAIRS);
+    });
 }
 
-cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* codes, const uint8_t* scales,
-                              const int32_t* offsets, const int32_t* perm, int k, int R, int rows, int N, int K, int G,
-                              float* dw, int accumulate, void* ws, uint64_t, cudaStream_t st) {
-    int32_t* flag = (int32_t*)ws;
-    cudaError_t e = launch_pdl(k_grad_head, dim3(1), dim3(1024), 0, st, offsets, G, R, flag);
+template <int MODE, bool CK>
+static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUtensorMap& b_map, cudaStream_t st) {
+    const int grid = grad_grid<MODE, CK>();
+    if (grid <= 0) return cudaErrorInvalidConfiguration;
+    const int pairs = grid / 2;
+    a.MT = (a.M + GG_TILE - 1) / GG_TILE;
+    a.NT = (a.N + GG_TILE - 1) / GG_TILE;
+    const long long tiles = (long long)a.G * a.MT * a.NT;
+    if (tiles >= (1LL << 30)) return cudaErrorInvalidValue;
+    a.tiles = (int)tiles;
+    a.full = a.tiles / pairs * pairs;
+    a.chunk_steps = GradCfg<MODE, CK>::CHUNK_STEPS;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(GG_THREADS);
+    cfg.dynamicSmemBytes = grad_smem<MODE, CK>();
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k_grad_gemm<MODE, CK>, a, a_map, b_map);
     count_launches(1);
-    if (e != cudaSuccess) return e;
-    const Bf16Rows a{(const __nv_bfloat16*)dy, lddy};
-    const CkptRows b{codes, scales, perm, k, rows, K, flag};
-    const StoreF32 c{dw, K, (long long)N * K, accumulate};
-    e = launch_pdl(k_grad_simt<Bf16Rows, CkptRows, StoreF32>, grad_grid(N, K, G), dim3(256), 0, st, a, b, c, offsets,
-                   R, N, K);
+    const int rem = a.tiles - a.full;
+    if (e != cudaSuccess || rem == 0 || a.R <= a.chunk_steps * GG_K) return e;
+    e = launch_pdl(k_grad_fixup, dim3((unsigned)rem, GG_TILE / 8), dim3(256), 0, st, a, pairs);
     count_launches(1);
     return e;
 }
 
+// Tensor map of `planes` row-major bf16 matrices [rows, cols] (rows ld apart,
+// matrices one behind the other): boxes of 64 columns with the 128-byte
+// swizzle; what lies outside reads as 0.
+static cudaError_t bf16_map(const void* p, long long ld, int rows, int cols, int planes, int box_rows,
+                            CUtensorMap* map) {
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+// Workspace: the error word (256 bytes), the parts of split tiles (where a tile
+// can be split: more rows than one chunk), and for the router the operands'
+// bf16 parts and the column sums.
+static size_t grad_part_bytes(int R, int chunk_steps) {
+    return R > chunk_steps * GG_K ? (size_t)GG_MAX_PAIRS * 2 * GG_TILE * GG_TILE * sizeof(float) : 0;
+}
+size_t wgrad_workspace_bytes(int R, int, int, int) {
+    return 256 + grad_part_bytes(R, GradCfg<GM_WGRAD, true>::CHUNK_STEPS);
+}
+
+struct RouterWs {
+    size_t wp, bias, dlp, part, total;
+};
+static RouterWs router_ws(int T, int H, int E) {
+    const size_t Ep = align_up(E, 8);
+    RouterWs L;
+    size_t o = 256;
+    L.wp = o; o += align_up(2 * 2 * (size_t)E * H, 256);
+    L.bias = o; o += align_up(sizeof(float) * kSplitMaxCtas * (size_t)E, 256);
+    L.dlp = o; o += align_up(3 * 2 * (size_t)T * Ep, 256);
+    L.part = o; o += grad_part_bytes(T, GradCfg<GM_RDW, true>::CHUNK_STEPS);
+    L.total = o;
+    return L;
+}
+size_t router_backward_workspace_bytes(int T, int H, int E) { return router_ws(T, H, E).total; }
+
+cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* codes, const uint8_t* scales,
+                              const int32_t* offsets, const int32_t* perm, int k, int R, int rows, int N, int K, int G,
+                              float* dw, int accumulate, void* ws, uint64_t wait_ns, cudaStream_t st) {
+    int32_t* flag = (int32_t*)ws;
+    cudaError_t e = launch_pdl(k_grad_head, dim3(1), dim3(1024), 0, st, offsets, G, R, flag);
+    count_launches(1);
+    if (e != cudaSuccess) return e;
+    if (R == 0) return accumulate ? cudaSuccess : cudaMemsetAsync(dw, 0, sizeof(float) * G * N * K, st);
+    CUtensorMap map;
+    e = bf16_map(dy, lddy, R, N, 1, GG_K, &map);
+    if (e != cudaSuccess) return e;
+    GradArgs a = {};
+    a.codes = codes;
+    a.scales = scales;
+    a.offsets = offsets;
+    a.perm = perm;
+    a.k_div = k;
+    a.xrows = rows;
+    a.R = R;
+    a.M = N;
+    a.N = K;
+    a.G = G;
+    a.c = dw;
+    a.accumulate = accumulate;
+    a.part = (float*)((char*)ws + 256);
+    a.flag = flag;
+    a.wait_ns = wait_ns;
+    return launch_grad<GM_WGRAD, true>(a, map, map, st);
+}
+
 cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t* codes, const uint8_t* scales,
                                    const float* w, int T, int H, int E, void* dx, float* dw, float* db, int accumulate,
-                                   void* ws, uint64_t, cudaStream_t st) {
+                                   void* ws, uint64_t wait_ns, cudaStream_t st) {
     int32_t* flag = (int32_t*)ws;
-    cudaError_t e = launch_pdl(k_grad_head, dim3(1), dim3(1024), 0, st, (const int32_t*)nullptr, 0, 0, flag);
-    count_launches(1);
-    if (e == cudaSuccess && dw) {
-        const F32Rows a{dl, E};
-        const StoreF32 c{dw, H, 0, accumulate};
-        if (x)
-            e = launch_pdl(k_grad_simt<F32Rows, Bf16Rows, StoreF32>, grad_grid(E, H, 1), dim3(256), 0, st, a,
-                           Bf16Rows{(const __nv_bfloat16*)x, H}, c, (const int32_t*)nullptr, T, E, H);
-        else
-            e = launch_pdl(k_grad_simt<F32Rows, CkptRows, StoreF32>, grad_grid(E, H, 1), dim3(256), 0, st, a,
-                           CkptRows{codes, scales, nullptr, 1, T, H, flag}, c, (const int32_t*)nullptr, T, E, H);
-        count_launches(1);
+    cudaError_t e = cudaSuccess;
+    if (T == 0) {
+        e = cudaMemsetAsync(flag, 0, sizeof(int32_t), st);
+        if (e == cudaSuccess && dw && !accumulate) e = cudaMemsetAsync(dw, 0, sizeof(float) * E * H, st);
+        if (e == cudaSuccess && db && !accumulate) e = cudaMemsetAsync(db, 0, sizeof(float) * E, st);
+        return e;
     }
-    if (e == cudaSuccess && dx && T > 0) {
-        e = launch_pdl(k_grad_simt<F32Cols, F32Rows, StoreBf16>, grad_grid(T, H, 1), dim3(256), 0, st, F32Cols{dl, E},
-                       F32Rows{w, H}, StoreBf16{(__nv_bfloat16*)dx, H}, (const int32_t*)nullptr, E, T, H);
-        count_launches(1);
+    const RouterWs L = router_ws(T, H, E);
+    char* b = (char*)ws;
+    const int Ep = (int)align_up(E, 8);
+    SplitArgs s = {};
+    s.dl = dl;
+    s.w = dx ? w : nullptr;
+    s.T = T;
+    s.E = E;
+    s.H = H;
+    s.Ep = Ep;
+    s.rows = std::max(16, (T + kSplitMaxCtas - 1) / kSplitMaxCtas);
+    s.ctas = (T + s.rows - 1) / s.rows;
+    s.parts = dw ? 3 : dx ? 2 : 0;
+    s.dlp = (__nv_bfloat16*)(b + L.dlp);
+    s.wp = (__nv_bfloat16*)(b + L.wp);
+    s.bias_part = db ? (float*)(b + L.bias) : nullptr;
+    s.flag = flag;
+    const int wctas = dx ? (int)std::min<size_t>(((size_t)E * H / 4 + kSplitThreads - 1) / kSplitThreads, 148 * 4) : 0;
+    e = launch_pdl(k_router_split, dim3((unsigned)(s.ctas + wctas)), dim3(kSplitThreads), 0, st, s);
+    count_launches(1);
+    GradArgs a = {};
+    a.G = 1;
+    a.N = H;
+    a.flag = flag;
+    a.wait_ns = wait_ns;
+    CUtensorMap a_map, b_map;
+    if (e == cudaSuccess && dw) {
+        e = bf16_map(s.dlp, Ep, T, Ep, 3, GG_K, &a_map);
+        b_map = a_map;
+        if (e == cudaSuccess && x) e = bf16_map(x, H, T, H, 1, GG_K, &b_map);
+        if (e != cudaSuccess) return e;
+        GradArgs d = a;
+        d.codes = codes;
+        d.scales = scales;
+        d.k_div = 1;
+        d.R = d.xrows = T;
+        d.M = E;
+        d.c = dw;
+        d.accumulate = accumulate;
+        d.part = (float*)(b + L.part);
+        e = x ? launch_grad<GM_RDW, false>(d, a_map, b_map, st) : launch_grad<GM_RDW, true>(d, a_map, b_map, st);
+    }
+    if (e == cudaSuccess && dx) {
+        e = bf16_map(s.dlp, Ep, T, Ep, 2, GG_HALF, &a_map);
+        if (e == cudaSuccess) e = bf16_map(s.wp, H, E, H, 2, GG_K, &b_map);
+        if (e != cudaSuccess) return e;
+        a.R = E;
+        a.M = T;
+        a.cb = (__nv_bfloat16*)dx;
+        e = launch_grad<GM_RDX, false>(a, a_map, b_map, st);
     }
     if (e == cudaSuccess && db) {
-        e = launch_pdl(k_grad_bias, dim3((unsigned)((E + 31) / 32)), dim3(1024), 0, st, dl, T, E, db, accumulate);
+        e = launch_pdl(k_router_bias, dim3((unsigned)((E + 31) / 32)), dim3(1024), 0, st, (const float*)s.bias_part,
+                       s.ctas, E, db, accumulate);
         count_launches(1);
     }
     return e;
