@@ -61,20 +61,6 @@ __device__ __forceinline__ void ckpt_values8(uint2 c, float s, float (&v)[8]) {
     }
 }
 
-// Eight codes times 2^(byte - 127) (a pair of bf16) as bf16: code and scale are
-// exact in bf16, the product is unless it falls below the normal range.
-__device__ __forceinline__ uint4 ckpt_bf16x8(uint2 c, uint32_t scale2) {
-    const uint32_t w[2] = {c.x, c.y};
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 p = e4m3x2_value((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-        const uint32_t b = __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x7632);   // truncation is exact
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(b), "r"(scale2));
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
 __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));

@@ -6,23 +6,28 @@
 // with bf16 operands and fp32 accumulation (tcgen05 kind::f16):
 //   GM_WGRAD   r = rows, A = dy (bf16), B = the checkpoint's values, which are
 //              exact in bf16 (4 significant bits times a power of two)
-//   GM_RDW     r = tokens, A = dlogits, B = x (bf16 or a checkpoint); dlogits
-//              is fp32 and enters as three bf16 parts of 8 bits each (exact):
-//              three products
+//   GM_RDW     r = tokens, A = dlogits, B = x (bf16 or a checkpoint's values);
+//              dlogits is fp32 and enters as three bf16 parts of 8 bits each
+//              (exact): three products
 //   GM_RDX     r = experts, A = dlogits, B = w_router, both fp32 with a bf16
 //              result: the leading two parts of each, three products (the
 //              smallest, low x low, is below 2^-16 of the terms)
-// k_router_split writes the fp32 operands' parts to the workspace first.
+// k_grad_prepare writes what is not bf16 as bf16 to the workspace first: the
+// checkpoint's values and the fp32 operands' parts.  Conversion inside the GEMM
+// (converter warps between a copy of the codes and the MMA) was built and
+// measured: it needs about 750 issue cycles per stage and scheduler against the
+// 512 of the stage's MMAs, 424 TFLOP/s in all (16384 x 4096 x 4096), where the
+// conversion in front costs 3 bytes of traffic per value.
 //
 // One SM pair (cluster of two CTAs, tcgen05 cta_group::2) per 256 x 256 tile of
 // C: the CTA of rank q supplies columns 128 q .. + 127 of A's and of B's tile
 // and holds rows 128 q .. + 127 of the accumulator.  A stage is 64 rows r.
-//   warp 0        bf16 operands by TMA (128-byte swizzle; "MN-major", the
+//   warp 0        operands by TMA (128-byte swizzle; "MN-major", the
 //                 contraction runs over smem rows, except A of GM_RDX)
 //   warp 1        (leader CTA) issues the MMAs
-//   warps 2, 3    checkpoint: codes by cp.async (rows through perm), scales
-//   warps 4-7     checkpoint: codes to bf16, into the swizzled stage.  Without
-//                 one, warp 4 passes "landed" on to the leader
+//   warp 2        GM_WGRAD through perm: checks the table
+//   warp 3        (other CTA) tells the leader that its stage is in place
+//   warps 4-7     GM_WGRAD: clear the rows behind a group's last one
 //   warps 8-15    epilogue, from two 256-column accumulators in TMEM
 // Work: pair p takes the tiles p, p + P, ... of the first floor(tiles / P) P
 // ones whole; the remaining tiles are cut into chunks of rows and dealt out
@@ -48,34 +53,32 @@ constexpr int GG_HALF = 128;            // per CTA: rows of A's tile, columns of
 constexpr int GG_K = 64;                // contraction rows per stage
 constexpr int GG_PLANE = GG_HALF * GG_K * 2;   // one operand part of a stage, per CTA
 constexpr int GG_BLOCK = GG_K * 128;    // 64 columns of an MN-major plane
-constexpr int GG_CONV_WARP0 = 4, GG_CONV_WARPS = 4, GG_EPI_WARP0 = 8, GG_EPI_WARPS = 8;
+constexpr int GG_TAIL_WARP0 = 4, GG_TAIL_WARPS = 4, GG_EPI_WARP0 = 8, GG_EPI_WARPS = 8;
 constexpr int GG_THREADS = 32 * (GG_EPI_WARP0 + GG_EPI_WARPS);
 constexpr int GG_MAX_PAIRS = 128;
-// Registers per thread: at launch, and of the three kinds of warpgroup after
+// Registers per thread: at launch, and of the two kinds of warpgroup after
 // setmaxnreg.  The epilogue holds 128 sums per thread.
-constexpr int GG_REGS = 128, GG_REGS_LOAD = 72, GG_REGS_CONV = 104, GG_REGS_EPI = 168;
-static_assert(GG_REGS_LOAD + GG_REGS_CONV + 2 * GG_REGS_EPI <= 4 * GG_REGS, "registers of the block");
+constexpr int GG_REGS = 128, GG_REGS_LOAD = 88, GG_REGS_EPI = 168;
+static_assert(2 * GG_REGS_LOAD + 2 * GG_REGS_EPI <= 4 * GG_REGS, "registers of the block");
 
-template <int MODE, bool CK>
+template <int MODE>
 struct GradCfg {
     static constexpr int AP = MODE == GM_WGRAD ? 1 : MODE == GM_RDW ? 3 : 2;   // parts of A
     static constexpr int BP = MODE == GM_RDX ? 2 : 1;
     static constexpr int OPS = (AP + BP) * GG_PLANE;
-    static constexpr int RAW = CK ? GG_K * GG_HALF + GG_K * 4 : 0;             // codes, scales (bf16 pairs)
-    static constexpr int STAGES = MODE == GM_WGRAD ? 5 : 3;
+    static constexpr int STAGES = MODE == GM_WGRAD ? 6 : 3;
     static constexpr int ACC_STEPS = MODE == GM_WGRAD ? 8 : MODE == GM_RDW ? 4 : 16;
     // rows per chunk of a split tile (a result of GM_RDX has at most 16 stages and is not split)
     static constexpr int CHUNK_STEPS = MODE == GM_WGRAD ? 16 : MODE == GM_RDW ? 8 : 16;
 };
 
-template <int MODE, bool CK>
+template <int MODE>
 struct GradShared {
-    uint8_t ops[GradCfg<MODE, CK>::STAGES][GradCfg<MODE, CK>::OPS];      // 1024-byte aligned
-    uint8_t raw[GradCfg<MODE, CK>::STAGES][CK ? GradCfg<MODE, CK>::RAW : 16];
-    uint64_t landed[GradCfg<MODE, CK>::STAGES];      // TMA bytes of this CTA
-    uint64_t raw_full[GradCfg<MODE, CK>::STAGES], raw_empty[GradCfg<MODE, CK>::STAGES];
-    uint64_t ready[GradCfg<MODE, CK>::STAGES];       // leader: both CTAs' operands are in place
-    uint64_t empty[GradCfg<MODE, CK>::STAGES];
+    uint8_t ops[GradCfg<MODE>::STAGES][GradCfg<MODE>::OPS];      // 1024-byte aligned
+    uint64_t landed[GradCfg<MODE>::STAGES];      // TMA bytes of this CTA
+    uint64_t tail[GradCfg<MODE>::STAGES];        // its rows behind the group are cleared
+    uint64_t peer[GradCfg<MODE>::STAGES];        // leader: the other CTA's operands are in place
+    uint64_t empty[GradCfg<MODE>::STAGES];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int32_t abort;
@@ -83,11 +86,9 @@ struct GradShared {
 };
 
 struct GradArgs {
-    const uint8_t* codes;      // checkpoint of B, or NULL
-    const uint8_t* scales;
     const int32_t* offsets;    // groups of rows, or NULL
-    const int32_t* perm;
-    int k_div, xrows;          // checkpoint row = perm[i] / k_div, below xrows
+    const int32_t* perm;       // checked here: perm[i] / k_div lies in [0, xrows); or NULL
+    int k_div, xrows;
     int R;                     // contraction rows of all groups
     int M, N, G;               // C is [G, M, N]
     int MT, NT, tiles, full, chunk_steps;
@@ -113,8 +114,14 @@ __device__ __forceinline__ uint32_t gg_peer(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// Arrival on the leader's barrier.  What it announces (operands in this CTA's
+// shared memory, an accumulator read out of this CTA's TMEM) is used only by
+// this SM's half of the MMA; it was written by TMA, whose barrier the caller has
+// seen complete, or fenced towards the async proxy by its writer.  So it needs
+// no cluster-wide fence, which .release.cluster would put here (1100 to 1600
+// cycles a stage, measured).
 __device__ __forceinline__ void gg_arrive(uint32_t bar, uint32_t rank) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(gg_peer(bar, rank)) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(gg_peer(bar, rank)) : "memory");
 }
 __device__ __forceinline__ void gg_commit(uint32_t bar) {
     asm volatile(
@@ -136,9 +143,6 @@ __device__ __forceinline__ void gg_tma(uint32_t dst, const CUtensorMap* map, int
         "[%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
-}
-__device__ __forceinline__ void gg_cp16(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 template <int REGS>
 __device__ __forceinline__ void gg_regs_down() {
@@ -274,15 +278,15 @@ struct Steps {
 };
 
 // ---- the kernel ----------------------------------------------------------------------
-template <int MODE, bool CK>
+template <int MODE>
 __global__ void __launch_bounds__(GG_THREADS, 1)
     k_grad_gemm(const __grid_constant__ GradArgs a, const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map) {
     pdl_begin();
-    using Cfg = GradCfg<MODE, CK>;
+    using Cfg = GradCfg<MODE>;
     constexpr int AP = Cfg::AP, BP = Cfg::BP, STAGES = Cfg::STAGES;
     extern __shared__ uint8_t gg_raw_smem[];
-    GradShared<MODE, CK>& sh =
-        *reinterpret_cast<GradShared<MODE, CK>*>(gg_raw_smem + ((1024u - (smem_u32(gg_raw_smem) & 1023u)) & 1023u));
+    GradShared<MODE>& sh =
+        *reinterpret_cast<GradShared<MODE>*>(gg_raw_smem + ((1024u - (smem_u32(gg_raw_smem) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = gg_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -290,9 +294,8 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sh.landed[s]), 1);
-            mbar_init(smem_u32(&sh.raw_full[s]), 128);      // two warps, a copy's and a plain arrival per lane
-            mbar_init(smem_u32(&sh.raw_empty[s]), GG_CONV_WARPS);
-            mbar_init(smem_u32(&sh.ready[s]), 2 * (CK ? GG_CONV_WARPS : 1));
+            mbar_init(smem_u32(&sh.tail[s]), GG_TAIL_WARPS);
+            mbar_init(smem_u32(&sh.peer[s]), 1);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -343,13 +346,13 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                      : "memory");
         raise_flag(a.flag, FLAG_TIMEOUT);
     };
-    auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_for<true>(bar, parity, a.wait_ns, abort); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_for<false>(bar, parity, a.wait_ns, abort); };
     // of a whole warp: its lanes go on or give up together
     auto warp_wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, !*abort && wait(bar, parity)) != 0;
     };
     auto final_wait = [&](uint32_t bar, uint32_t parity) {
-        if (!mbar_wait_for<true>(bar, parity, a.wait_ns, nullptr)) raise_flag(a.flag, FLAG_TIMEOUT);
+        if (!mbar_wait_for<false>(bar, parity, a.wait_ns, nullptr)) raise_flag(a.flag, FLAG_TIMEOUT);
     };
     const Walk walk0(a, sh.rem_pre, pair, pairs);
     int stage = 0;
@@ -361,12 +364,26 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         }
     };
 
-    if (warp < GG_CONV_WARP0) {
+    // Stages with rows behind their group's last one (the last stage of a group
+    // with another row count than a multiple of 64): dy and x of other rows have
+    // landed there and are cleared (rows behind R read as 0).  tails: parity of each stage's next clearing.
+    uint32_t tails = 0;
+    auto has_tail = [&](const Segment& s, int st) {
+        return MODE == GM_WGRAD && s.r1 < a.R && s.r1 - s.r0 - st * GG_K < GG_K;
+    };
+    auto wait_tail = [&](const Segment& s, int st) {
+        if (!has_tail(s, st)) return true;
+        const uint32_t p = tails >> stage & 1u;
+        tails ^= 1u << stage;
+        return wait(smem_u32(&sh.tail[stage]), p);
+    };
+
+    if (warp < GG_TAIL_WARP0) {
         gg_regs_down<GG_REGS_LOAD>();
         if (warp == 0 && lane == 0) {
             // ---------------- bf16 operands by TMA ----------------
             uint32_t filled = 0, parity = 0;      // bit s: stage s has a copy, and its phase
-            constexpr uint32_t bytes = (AP + (CK ? 0 : BP)) * GG_PLANE;
+            constexpr uint32_t bytes = (AP + BP) * GG_PLANE;
             for (Steps s(walk0); s.on; s.advance()) {
                 if (*abort || !wait(smem_u32(&sh.empty[stage]), phase ^ 1u)) {
                     give_up();
@@ -386,12 +403,10 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                         gg_tma(dst + GG_BLOCK, &a_map, m + 64, r, p, bar);
                     }
                 }
-                if (!CK) {
 #pragma unroll
-                    for (int p = 0; p < BP; ++p, dst += GG_PLANE) {
-                        gg_tma(dst, &b_map, n, r, p, bar);
-                        gg_tma(dst + GG_BLOCK, &b_map, n + 64, r, p, bar);
-                    }
+                for (int p = 0; p < BP; ++p, dst += GG_PLANE) {
+                    gg_tma(dst, &b_map, n, r, p, bar);
+                    gg_tma(dst + GG_BLOCK, &b_map, n + 64, r, p, bar);
                 }
                 filled |= 1u << stage;
                 parity = (parity & ~(1u << stage)) | (phase << stage);
@@ -419,7 +434,8 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                         tc_fence_after();
                         const uint32_t d = tmem + buf * GG_TILE;
                         for (int s = st; s < st1; ++s) {
-                            if (!wait(smem_u32(&sh.ready[stage]), phase)) {
+                            if (!wait(smem_u32(&sh.landed[stage]), phase) || !wait_tail(seg, s) ||
+                                !wait(smem_u32(&sh.peer[stage]), phase)) {
                                 give_up();
                                 ok = false;
                                 break;
@@ -460,124 +476,44 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             }
             // every MMA is done before either CTA frees its TMEM
             final_wait(smem_u32(&sh.drain), 0);
-        } else if (CK && warp >= 2) {
-            // ---------------- checkpoint codes and scales ----------------
-            // Lane = row of this warp's 32; row indices are resolved two stages
-            // ahead and scale bytes read one stage ahead of the copies.
-            const int half = 32 * (warp - 2);
-            auto read_perm = [&](const Steps& s) {
-                const int i = s.seg.r0 + s.st * GG_K + half + lane;
-                if (!s.on || i >= s.seg.r1 || s.seg.n0 + GG_HALF * (int)rank >= a.N) return -1;
-                return a.perm ? __ldg(a.perm + i) : i;
-            };
-            // the checkpoint row of a table entry (-1: a row of zeros)
-            auto resolve = [&](const Steps& s, int v) {
-                const int i = s.seg.r0 + s.st * GG_K + half + lane;
-                if (!s.on || i >= s.seg.r1 || s.seg.n0 + GG_HALF * (int)rank >= a.N) return -1;
-                return a.perm ? checked_index(v < 0 ? v : v / a.k_div, a.xrows, a.flag) : v;
-            };
-            auto read_scale = [&](const Steps& s, int x) -> uint32_t {
-                if (x < 0) return 0u;
-                return __ldg(a.scales + (size_t)x * (a.N >> 7) + ((s.seg.n0 >> 7) + rank));
-            };
-            Steps s0(walk0);
-            Steps s2(s0);
-            int x0 = resolve(s0, read_perm(s0));
-            uint32_t b0 = read_scale(s0, x0);
-            s2.advance();
-            Steps s1(s2);
-            int v1 = read_perm(s1);
-            for (; s0.on;) {
-                s2.advance();
-                const int x1 = resolve(s1, v1);
-                const uint32_t b1 = read_scale(s1, x1);
-                const int v2 = read_perm(s2);
-                if (!warp_wait(smem_u32(&sh.raw_empty[stage]), phase ^ 1u)) {
+        } else if (MODE == GM_WGRAD && warp == 2 && a.perm) {
+            // (k_grad_prepare reads row 0 for a bad entry; the error word is this
+            // call's only from the second kernel on)
+            for (long long i = blockIdx.x * 32 + lane; i < a.R; i += gridDim.x * 32) {
+                const int v = __ldg(a.perm + i);
+                checked_index(v < 0 ? v : v / a.k_div, a.xrows, a.flag);
+            }
+        } else if (warp == 3 && lane == 0 && rank == 1) {
+            // ---------------- "in place" to the leader ----------------
+            for (Steps s(walk0); s.on; s.advance()) {
+                if (!wait(smem_u32(&sh.landed[stage]), phase) || !wait_tail(s.seg, s.st)) {
                     give_up();
                     break;
                 }
-                const uint32_t raw = smem_u32(sh.raw[stage]), bar = smem_u32(&sh.raw_full[stage]);
-                {
-                    // 2^(byte - 127) as a pair of bf16 (exact)
-                    const uint32_t h = __float_as_uint(ckpt_scale(b0)) >> 16;
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(raw + GG_K * GG_HALF + 4 * (half + lane)),
-                                 "r"(h | h << 16)
-                                 : "memory");
-                }
-                const int n = s0.seg.n0 + GG_HALF * (int)rank;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int row = 4 * j + (lane >> 3);
-                    const int x = __shfl_sync(0xffffffffu, x0, row);
-                    const uint8_t* p = x >= 0 ? a.codes + (size_t)x * a.N + n + 16 * (lane & 7) : a.codes;
-                    gg_cp16(raw + (half + row) * GG_HALF + 16 * (lane & 7), p, x >= 0);
-                }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-                mbar_arrive(bar);
+                gg_arrive(smem_u32(&sh.peer[stage]), 0);
                 next_stage();
-                s0 = s1;
-                s1 = s2;
-                x0 = x1;
-                b0 = b1;
-                v1 = v2;
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
     } else if (warp < GG_EPI_WARP0) {
-        gg_regs_down<GG_REGS_CONV>();
-        if (CK) {
-            // ---------------- checkpoint codes to bf16 ----------------
-            // Thread t: 8 codes (8-byte column t % 16) of the rows t / 16 + 8 u.
-            const int t = threadIdx.x - 32 * GG_CONV_WARP0, c = t & 15, rr = t >> 4;
-            const uint32_t doff = (uint32_t)(AP * GG_PLANE + (c >> 3) * GG_BLOCK);
+        gg_regs_down<GG_REGS_LOAD>();
+        if (MODE == GM_WGRAD && a.offsets) {
+            // ---------------- rows behind a group's last one ----------------
+            const int t = threadIdx.x - 32 * GG_TAIL_WARP0;
             for (Steps s(walk0); s.on; s.advance()) {
-                if (!warp_wait(smem_u32(&sh.raw_full[stage]), phase)) {
-                    give_up();
-                    break;
-                }
-                const uint8_t* raw = sh.raw[stage];
-                uint2 q[8];
-                uint32_t f[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    q[u] = *reinterpret_cast<const uint2*>(raw + (rr + 8 * u) * GG_HALF + 8 * c);
-                    f[u] = *reinterpret_cast<const uint32_t*>(raw + GG_K * GG_HALF + 4 * (rr + 8 * u));
-                }
-                if (!warp_wait(smem_u32(&sh.empty[stage]), phase ^ 1u)) {
-                    give_up();
-                    break;
-                }
-                const uint32_t dst = smem_u32(sh.ops[stage]);
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    gg_st16(dst + doff + gg_swz(rr + 8 * u, c & 7), ckpt_bf16x8(q[u], f[u]));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[stage]));
                 if (!warp_wait(smem_u32(&sh.landed[stage]), phase)) {
                     give_up();
                     break;
                 }
-                if (MODE == GM_WGRAD) {
-                    // rows of the next group in the last stage of this one: dy must not
-                    // meet the zeros of B there (0 x NaN)
+                if (has_tail(s.seg, s.st)) {
                     const int valid = s.seg.r1 - s.seg.r0 - s.st * GG_K;
-                    if (valid < GG_K)
-                        for (int i = t; i < GG_K * 16; i += 32 * GG_CONV_WARPS)
-                            if ((i >> 3 & (GG_K - 1)) >= valid) gg_st16(dst + i * 16, make_uint4(0u, 0u, 0u, 0u));
+                    const uint32_t dst = smem_u32(sh.ops[stage]);
+                    for (int i = t; i < Cfg::OPS / 16; i += 32 * GG_TAIL_WARPS)
+                        if ((i >> 3 & (GG_K - 1)) >= valid) gg_st16(dst + i * 16, make_uint4(0u, 0u, 0u, 0u));
+                    gg_fence_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.tail[stage]));
                 }
-                gg_fence_async();
-                __syncwarp();
-                if (lane == 0) gg_arrive(smem_u32(&sh.ready[stage]), 0);
-                next_stage();
-            }
-        } else if (warp == GG_CONV_WARP0 && lane == 0) {
-            for (Steps s(walk0); s.on; s.advance()) {
-                if (*abort || !wait(smem_u32(&sh.landed[stage]), phase)) {
-                    give_up();
-                    break;
-                }
-                gg_arrive(smem_u32(&sh.ready[stage]), 0);
                 next_stage();
             }
         }
@@ -741,18 +677,6 @@ __global__ void __launch_bounds__(256) k_grad_fixup(GradArgs a, int pairs) {
     }
 }
 
-// First kernel of a call: clears the error word, or raises FLAG_BOUNDS there
-// when the group offsets do not ascend within [0, R].
-__global__ void __launch_bounds__(1024) k_grad_head(const int32_t* offsets, int G, int R, int32_t* flag) {
-    pdl_begin();
-    bool bad = false;
-    if (offsets)
-        for (int g = threadIdx.x; g < G; g += blockDim.x)
-            bad |= offsets[g] < 0 || offsets[g + 1] < offsets[g] || offsets[g + 1] > R;
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *flag = bad ? FLAG_BOUNDS : 0;
-}
-
 // ---- the router's fp32 operands as bf16 parts --------------------------------------
 // v = h + m + l, each with 8 significant bits: h and m rounded to nearest, l
 // exact (24 = 8 + 8 + 8 bits).  An infinity or NaN is its own first part.
@@ -768,27 +692,101 @@ __device__ __forceinline__ void split3(float v, float& h, float& m, float& l) {
 constexpr int kSplitThreads = 256;
 constexpr int kSplitMaxCtas = 148 * 4;
 
-struct SplitArgs {
+// What a call needs as bf16 in its workspace.  The grid's CTAs take the parts
+// in turn: dlogits, w_router, the checkpoint.
+struct PrepareArgs {
     const float* dl;         // [T, E]
-    const float* w;          // [E, H] or NULL
+    const float* w;          // [E, H]
     int T, E, H, Ep;         // Ep: E rounded up to 8
     int rows;                // tokens per CTA
-    int ctas;                // CTAs of dl; the others take w
+    int dl_ctas, w_ctas;
     int parts;               // of dl: 3, 2, or 0 (none written)
     __nv_bfloat16* dlp;      // [3][T][Ep]
     __nv_bfloat16* wp;       // [2][E][H]
-    float* bias_part;        // [ctas][E] column sums, or NULL
+    float* bias_part;        // [dl_ctas][E] column sums, or NULL
+    const uint8_t* codes;    // checkpoint [.., K], `items` groups of 8 codes
+    const uint8_t* scales;
+    long long items;
+    int K;
+    const int32_t* perm;     // row i from row perm[i] / k_div below xrows, or NULL
+    int k_div, xrows;
+    __nv_bfloat16* xb;
+    const int32_t* offsets;  // checked by the first CTA, or NULL
+    int G, R;
     int32_t* flag;
 };
 
-// Thread: 4 neighbouring columns of every (256 / (Ep / 4))-th row of the CTA's.
-// Also clears the call's error word (the first kernel of a call).
-__global__ void __launch_bounds__(kSplitThreads) k_router_split(SplitArgs a) {
+// The first CTA also clears the call's error word, or raises FLAG_BOUNDS there
+// when the group offsets do not ascend within [0, R].
+__global__ void __launch_bounds__(kSplitThreads) k_grad_prepare(PrepareArgs a) {
     pdl_begin();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.flag = 0;
-    if ((int)blockIdx.x >= a.ctas) {
-        const size_t n4 = (size_t)a.E * a.H / 4, step = (size_t)(gridDim.x - a.ctas) * kSplitThreads;
-        for (size_t i = (size_t)(blockIdx.x - a.ctas) * kSplitThreads + threadIdx.x; i < n4; i += step) {
+    if (blockIdx.x == 0) {
+        bool bad = false;
+        if (a.offsets)
+            for (int g = threadIdx.x; g < a.G; g += kSplitThreads)
+                bad |= a.offsets[g] < 0 || a.offsets[g + 1] < a.offsets[g] || a.offsets[g + 1] > a.R;
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *a.flag = bad ? FLAG_BOUNDS : 0;
+    }
+    int b = blockIdx.x;
+    if (b < a.dl_ctas) {
+        // Thread: 4 neighbouring columns of every (256 / (Ep / 4))-th row of the CTA's.
+        const int c4 = a.Ep / 4, c = 4 * ((int)threadIdx.x % c4), rg = (int)threadIdx.x / c4, rgs = kSplitThreads / c4;
+        const int t0 = b * a.rows, t1 = min(a.T, t0 + a.rows);
+        const bool vec = (a.E & 3) == 0;
+        float sum[4] = {};
+        if (rg < rgs) {
+#pragma unroll 4
+            for (int t = t0 + rg; t < t1; t += rgs) {
+                const float* p = a.dl + (size_t)t * a.E + c;
+                float v[4] = {};
+                if (vec) {
+                    if (c < a.E) {
+                        const float4 q = __ldg(reinterpret_cast<const float4*>(p));
+                        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (c + j < a.E) v[j] = __ldg(p + j);
+                }
+                float h[4], m[4], l[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sum[j] += v[j];
+                    split3(v[j], h[j], m[j], l[j]);
+                }
+                if (a.parts) {
+                    __nv_bfloat16* o = a.dlp + (size_t)t * a.Ep + c;
+                    const size_t plane = (size_t)a.T * a.Ep;
+                    *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(h[0], h[1]), bf16x2_rn(h[2], h[3]));
+                    *reinterpret_cast<uint2*>(o + plane) = make_uint2(bf16x2_rn(m[0], m[1]), bf16x2_rn(m[2], m[3]));
+                    if (a.parts == 3)
+                        *reinterpret_cast<uint2*>(o + 2 * plane) = make_uint2(bf16x2_rn(l[0], l[1]), bf16x2_rn(l[2], l[3]));
+                }
+            }
+        }
+        if (a.bias_part) {
+            // the row groups' sums, added in order
+            __shared__ float s[kSplitThreads][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[threadIdx.x][j] = sum[j];
+            __syncthreads();
+            if (rg == 0) {
+                for (int g = 1; g < rgs; ++g)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sum[j] += s[g * c4 + threadIdx.x][j];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c + j < a.E) a.bias_part[(size_t)b * a.E + c + j] = sum[j];
+            }
+        }
+        return;
+    }
+    b -= a.dl_ctas;
+    if (b < a.w_ctas) {
+        const size_t n4 = (size_t)a.E * a.H / 4, step = (size_t)a.w_ctas * kSplitThreads;
+        for (size_t i = (size_t)b * kSplitThreads + threadIdx.x; i < n4; i += step) {
             const float4 v = __ldg(reinterpret_cast<const float4*>(a.w) + i);
             float h[4], m[4], l;
             split3(v.x, h[0], m[0], l);
@@ -800,56 +798,40 @@ __global__ void __launch_bounds__(kSplitThreads) k_router_split(SplitArgs a) {
         }
         return;
     }
-    const int c4 = a.Ep / 4, c = 4 * ((int)threadIdx.x % c4), rg = (int)threadIdx.x / c4, rgs = kSplitThreads / c4;
-    const int t0 = blockIdx.x * a.rows, t1 = min(a.T, t0 + a.rows);
-    const bool vec = (a.E & 3) == 0;
-    float sum[4] = {};
-    if (rg < rgs) {
-#pragma unroll 4
-        for (int t = t0 + rg; t < t1; t += rgs) {
-            const float* p = a.dl + (size_t)t * a.E + c;
-            float v[4] = {};
-            if (vec) {
-                if (c < a.E) {
-                    const float4 q = __ldg(reinterpret_cast<const float4*>(p));
-                    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-                }
-            } else {
+    b -= a.w_ctas;
+    // The checkpoint's values, 8 codes per item.
+    constexpr int U = 4;
+    const int K8 = a.K / 8;
+    const long long stride = (long long)(gridDim.x - a.dl_ctas - a.w_ctas) * kSplitThreads;
+    for (long long i0 = (long long)b * kSplitThreads + threadIdx.x; i0 < a.items; i0 += stride * U) {
+        uint2 c[U];
+        uint32_t s[U];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (c + j < a.E) v[j] = __ldg(p + j);
+        for (int u = 0; u < U; ++u) {
+            const long long i = i0 + u * stride;
+            long long src = i;
+            if (i >= a.items) continue;
+            if (a.perm) {
+                const int r = (int)(i / K8), v = __ldg(a.perm + r);
+                const int x = v < 0 ? 0 : v / a.k_div;
+                src = (long long)(x < a.xrows ? x : 0) * K8 + (i - (long long)r * K8);    // (bad entries: row 0)
             }
-            float h[4], m[4], l[4];
+            c[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + src * 8));
+            s[u] = __ldg(a.scales + (src >> 4));
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sum[j] += v[j];
-                split3(v[j], h[j], m[j], l[j]);
-            }
-            if (a.parts) {
-                __nv_bfloat16* o = a.dlp + (size_t)t * a.Ep + c;
-                const size_t plane = (size_t)a.T * a.Ep;
-                *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(h[0], h[1]), bf16x2_rn(h[2], h[3]));
-                *reinterpret_cast<uint2*>(o + plane) = make_uint2(bf16x2_rn(m[0], m[1]), bf16x2_rn(m[2], m[3]));
-                if (a.parts == 3)
-                    *reinterpret_cast<uint2*>(o + 2 * plane) = make_uint2(bf16x2_rn(l[0], l[1]), bf16x2_rn(l[2], l[3]));
-            }
+        for (int u = 0; u < U; ++u) {
+            const long long i = i0 + u * stride;
+            if (i >= a.items) break;
+            float v[8];
+            ckpt_values8(c[u], ckpt_scale(s[u]), v);
+            reinterpret_cast<uint4*>(a.xb)[i] = bf16x8_rn(v);
         }
     }
-    if (a.bias_part) {
-        // the row groups' sums, added in order
-        __shared__ float s[kSplitThreads][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[threadIdx.x][j] = sum[j];
-        __syncthreads();
-        if (rg == 0) {
-            for (int g = 1; g < rgs; ++g)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sum[j] += s[g * c4 + threadIdx.x][j];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c + j < a.E) a.bias_part[(size_t)blockIdx.x * a.E + c + j] = sum[j];
-        }
-    }
+}
+
+static unsigned prepare_ctas(long long items) {
+    return (unsigned)std::min<long long>((items + 4 * kSplitThreads - 1) / (4 * kSplitThreads), 148 * 32);
 }
 
 // dbias: the CTAs' column sums, warps take every 32nd, then in warp order.
@@ -871,16 +853,16 @@ __global__ void __launch_bounds__(1024) k_router_bias(const float* __restrict__ 
 }
 
 // ---- host -----------------------------------------------------------------------------
-template <int MODE, bool CK>
-static size_t grad_smem() { return sizeof(GradShared<MODE, CK>) + 1024; }
+template <int MODE>
+static size_t grad_smem() { return sizeof(GradShared<MODE>) + 1024; }
 
 // CTAs of the kernel that can be resident as pairs (a persistent grid).
-template <int MODE, bool CK>
+template <int MODE>
 static int grad_grid() {
     static PerContext cache;
     return cache.get([] {
-        auto kernel = k_grad_gemm<MODE, CK>;
-        const size_t smem = grad_smem<MODE, CK>();
+        auto kernel = k_grad_gemm<MODE>;
+        const size_t smem = grad_smem<MODE>();
         int dev = 0, sms = 0, clusters = 0;
         cudaFuncAttributes fa;
         if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -906,9 +888,9 @@ static int grad_grid() {
     });
 }
 
-template <int MODE, bool CK>
+template <int MODE>
 static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUtensorMap& b_map, cudaStream_t st) {
-    const int grid = grad_grid<MODE, CK>();
+    const int grid = grad_grid<MODE>();
     if (grid <= 0) return cudaErrorInvalidConfiguration;
     const int pairs = grid / 2;
     a.MT = (a.M + GG_TILE - 1) / GG_TILE;
@@ -917,11 +899,11 @@ static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUten
     if (tiles >= (1LL << 30)) return cudaErrorInvalidValue;
     a.tiles = (int)tiles;
     a.full = a.tiles / pairs * pairs;
-    a.chunk_steps = GradCfg<MODE, CK>::CHUNK_STEPS;
+    a.chunk_steps = GradCfg<MODE>::CHUNK_STEPS;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(GG_THREADS);
-    cfg.dynamicSmemBytes = grad_smem<MODE, CK>();
+    cfg.dynamicSmemBytes = grad_smem<MODE>();
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -932,7 +914,7 @@ static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUten
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k_grad_gemm<MODE, CK>, a, a_map, b_map);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k_grad_gemm<MODE>, a, a_map, b_map);
     count_launches(1);
     const int rem = a.tiles - a.full;
     if (e != cudaSuccess || rem == 0 || a.R <= a.chunk_steps * GG_K) return e;
@@ -941,15 +923,11 @@ static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUten
     return e;
 }
 
-// Tensor map of `planes` row-major bf16 matrices [rows, cols] (rows ld apart,
-// matrices one behind the other): boxes of 64 columns with the 128-byte
-// swizzle; what lies outside reads as 0.
-static cudaError_t bf16_map(const void* p, long long ld, int rows, int cols, int planes, int box_rows,
-                            CUtensorMap* map) {
-    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static const Encode encode = [] {
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encode_tiled() {
+    static const EncodeTiled encode = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
@@ -957,8 +935,17 @@ static cudaError_t bf16_map(const void* p, long long ld, int rows, int cols, int
             cudaGetLastError();
             f = nullptr;
         }
-        return reinterpret_cast<Encode>(f);
+        return reinterpret_cast<EncodeTiled>(f);
     }();
+    return encode;
+}
+
+// Tensor map of `planes` row-major bf16 matrices [rows, cols] (rows ld apart,
+// matrices one behind the other): boxes of 64 columns with the 128-byte
+// swizzle; what lies outside reads as 0.
+static cudaError_t bf16_map(const void* p, long long ld, int rows, int cols, int planes, int box_rows,
+                            CUtensorMap* map) {
+    const EncodeTiled encode = encode_tiled();
     if (!encode) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
@@ -970,18 +957,18 @@ static cudaError_t bf16_map(const void* p, long long ld, int rows, int cols, int
                : cudaErrorInvalidValue;
 }
 
-// Workspace: the error word (256 bytes), the parts of split tiles (where a tile
-// can be split: more rows than one chunk), and for the router the operands'
-// bf16 parts and the column sums.
+// Workspace: the error word (256 bytes), the operands as bf16, the parts of
+// split tiles (where a tile can be split: more rows than one chunk).
 static size_t grad_part_bytes(int R, int chunk_steps) {
     return R > chunk_steps * GG_K ? (size_t)GG_MAX_PAIRS * 2 * GG_TILE * GG_TILE * sizeof(float) : 0;
 }
-size_t wgrad_workspace_bytes(int R, int, int, int) {
-    return 256 + grad_part_bytes(R, GradCfg<GM_WGRAD, true>::CHUNK_STEPS);
+static size_t wgrad_part_offset(int R, int K) { return 256 + align_up(2 * (size_t)R * K, 256); }
+size_t wgrad_workspace_bytes(int R, int, int K, int) {
+    return wgrad_part_offset(R, K) + grad_part_bytes(R, GradCfg<GM_WGRAD>::CHUNK_STEPS);
 }
 
 struct RouterWs {
-    size_t wp, bias, dlp, part, total;
+    size_t wp, bias, dlp, xb, part, total;
 };
 static RouterWs router_ws(int T, int H, int E) {
     const size_t Ep = align_up(E, 8);
@@ -990,7 +977,8 @@ static RouterWs router_ws(int T, int H, int E) {
     L.wp = o; o += align_up(2 * 2 * (size_t)E * H, 256);
     L.bias = o; o += align_up(sizeof(float) * kSplitMaxCtas * (size_t)E, 256);
     L.dlp = o; o += align_up(3 * 2 * (size_t)T * Ep, 256);
-    L.part = o; o += grad_part_bytes(T, GradCfg<GM_RDW, true>::CHUNK_STEPS);
+    L.xb = o; o += align_up(2 * (size_t)T * H, 256);
+    L.part = o; o += grad_part_bytes(T, GradCfg<GM_RDW>::CHUNK_STEPS);
     L.total = o;
     return L;
 }
@@ -1000,16 +988,28 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
                               const int32_t* offsets, const int32_t* perm, int k, int R, int rows, int N, int K, int G,
                               float* dw, int accumulate, void* ws, uint64_t wait_ns, cudaStream_t st) {
     int32_t* flag = (int32_t*)ws;
-    cudaError_t e = launch_pdl(k_grad_head, dim3(1), dim3(1024), 0, st, offsets, G, R, flag);
+    cudaError_t e = cudaSuccess;
+    PrepareArgs s = {};
+    s.codes = codes;
+    s.scales = scales;
+    s.items = (long long)R * (K / 8);
+    s.K = K;
+    s.perm = perm;
+    s.k_div = k;
+    s.xrows = rows;
+    s.xb = (__nv_bfloat16*)((char*)ws + 256);
+    s.offsets = offsets;
+    s.G = G;
+    s.R = R;
+    s.flag = flag;
+    e = launch_pdl(k_grad_prepare, dim3(std::max(1u, prepare_ctas(s.items))), dim3(kSplitThreads), 0, st, s);
     count_launches(1);
-    if (e != cudaSuccess) return e;
-    if (R == 0) return accumulate ? cudaSuccess : cudaMemsetAsync(dw, 0, sizeof(float) * G * N * K, st);
-    CUtensorMap map;
-    e = bf16_map(dy, lddy, R, N, 1, GG_K, &map);
+    if (e == cudaSuccess && R == 0) return accumulate ? e : cudaMemsetAsync(dw, 0, sizeof(float) * G * N * K, st);
+    CUtensorMap a_map, b_map;
+    if (e == cudaSuccess) e = bf16_map(dy, lddy, R, N, 1, GG_K, &a_map);
+    if (e == cudaSuccess) e = bf16_map(s.xb, K, R, K, 1, GG_K, &b_map);
     if (e != cudaSuccess) return e;
     GradArgs a = {};
-    a.codes = codes;
-    a.scales = scales;
     a.offsets = offsets;
     a.perm = perm;
     a.k_div = k;
@@ -1020,10 +1020,10 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
     a.G = G;
     a.c = dw;
     a.accumulate = accumulate;
-    a.part = (float*)((char*)ws + 256);
+    a.part = (float*)((char*)ws + wgrad_part_offset(R, K));
     a.flag = flag;
     a.wait_ns = wait_ns;
-    return launch_grad<GM_WGRAD, true>(a, map, map, st);
+    return launch_grad<GM_WGRAD>(a, a_map, b_map, st);
 }
 
 cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t* codes, const uint8_t* scales,
@@ -1040,22 +1040,28 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
     const RouterWs L = router_ws(T, H, E);
     char* b = (char*)ws;
     const int Ep = (int)align_up(E, 8);
-    SplitArgs s = {};
+    PrepareArgs s = {};
     s.dl = dl;
-    s.w = dx ? w : nullptr;
+    s.w = w;
     s.T = T;
     s.E = E;
     s.H = H;
     s.Ep = Ep;
     s.rows = std::max(16, (T + kSplitMaxCtas - 1) / kSplitMaxCtas);
-    s.ctas = (T + s.rows - 1) / s.rows;
+    s.dl_ctas = (T + s.rows - 1) / s.rows;
+    s.w_ctas = dx ? (int)std::min<size_t>(((size_t)E * H / 4 + kSplitThreads - 1) / kSplitThreads, 148 * 4) : 0;
     s.parts = dw ? 3 : dx ? 2 : 0;
     s.dlp = (__nv_bfloat16*)(b + L.dlp);
     s.wp = (__nv_bfloat16*)(b + L.wp);
     s.bias_part = db ? (float*)(b + L.bias) : nullptr;
+    s.codes = codes;
+    s.scales = scales;
+    s.items = dw && codes ? (long long)T * (H / 8) : 0;
+    s.K = H;
+    s.xb = (__nv_bfloat16*)(b + L.xb);
     s.flag = flag;
-    const int wctas = dx ? (int)std::min<size_t>(((size_t)E * H / 4 + kSplitThreads - 1) / kSplitThreads, 148 * 4) : 0;
-    e = launch_pdl(k_router_split, dim3((unsigned)(s.ctas + wctas)), dim3(kSplitThreads), 0, st, s);
+    e = launch_pdl(k_grad_prepare, dim3((unsigned)(s.dl_ctas + s.w_ctas) + prepare_ctas(s.items)), dim3(kSplitThreads), 0,
+                   st, s);
     count_launches(1);
     GradArgs a = {};
     a.G = 1;
@@ -1065,19 +1071,15 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
     CUtensorMap a_map, b_map;
     if (e == cudaSuccess && dw) {
         e = bf16_map(s.dlp, Ep, T, Ep, 3, GG_K, &a_map);
-        b_map = a_map;
-        if (e == cudaSuccess && x) e = bf16_map(x, H, T, H, 1, GG_K, &b_map);
+        if (e == cudaSuccess) e = bf16_map(x ? x : s.xb, H, T, H, 1, GG_K, &b_map);
         if (e != cudaSuccess) return e;
         GradArgs d = a;
-        d.codes = codes;
-        d.scales = scales;
-        d.k_div = 1;
-        d.R = d.xrows = T;
+        d.R = T;
         d.M = E;
         d.c = dw;
         d.accumulate = accumulate;
         d.part = (float*)(b + L.part);
-        e = x ? launch_grad<GM_RDW, false>(d, a_map, b_map, st) : launch_grad<GM_RDW, true>(d, a_map, b_map, st);
+        e = launch_grad<GM_RDW>(d, a_map, b_map, st);
     }
     if (e == cudaSuccess && dx) {
         e = bf16_map(s.dlp, Ep, T, Ep, 2, GG_HALF, &a_map);
@@ -1086,11 +1088,11 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
         a.R = E;
         a.M = T;
         a.cb = (__nv_bfloat16*)dx;
-        e = launch_grad<GM_RDX, false>(a, a_map, b_map, st);
+        e = launch_grad<GM_RDX>(a, a_map, b_map, st);
     }
     if (e == cudaSuccess && db) {
         e = launch_pdl(k_router_bias, dim3((unsigned)((E + 31) / 32)), dim3(1024), 0, st, (const float*)s.bias_part,
-                       s.ctas, E, db, accumulate);
+                       s.dl_ctas, E, db, accumulate);
         count_launches(1);
     }
     return e;
