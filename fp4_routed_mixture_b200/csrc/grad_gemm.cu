@@ -26,7 +26,6 @@
 //                 contraction runs over smem rows, except A of GM_RDX)
 //   warp 1        (leader CTA) issues the MMAs
 //   warp 2        GM_WGRAD through perm: checks the table
-//   warp 3        (other CTA) tells the leader that its stage is in place
 //   warps 4-7     GM_WGRAD: clear the rows behind a group's last one
 //   warps 8-15    epilogue, from two 256-column accumulators in TMEM
 // Work: pair p takes the tiles p, p + P, ... of the first floor(tiles / P) P
@@ -37,7 +36,7 @@
 // The tensor cores truncate when they add to the fp32 accumulator, always
 // towards zero: about 7e-9 of the result per MMA (measured: 1.2e-6 after 256
 // of them, against 6e-7 of an fp32 sum in CUDA cores).  So an accumulator is
-// drained every ACC_STEPS stages and added up in the epilogue's registers,
+// drained every ACC_STEPS stages (1024 rows in GM_WGRAD) and added up in the epilogue's registers,
 // rounding to nearest.
 #include "ckpt.cuh"
 #include "kernels.cuh"
@@ -55,6 +54,7 @@ constexpr int GG_PLANE = GG_HALF * GG_K * 2;   // one operand part of a stage, p
 constexpr int GG_BLOCK = GG_K * 128;    // 64 columns of an MN-major plane
 constexpr int GG_TAIL_WARP0 = 4, GG_TAIL_WARPS = 4, GG_EPI_WARP0 = 8, GG_EPI_WARPS = 8;
 constexpr int GG_THREADS = 32 * (GG_EPI_WARP0 + GG_EPI_WARPS);
+constexpr int GG_OUT = 32 * 128;
 constexpr int GG_MAX_PAIRS = 128;
 // Registers per thread: at launch, and of the two kinds of warpgroup after
 // setmaxnreg.  The epilogue holds 128 sums per thread.
@@ -67,7 +67,7 @@ struct GradCfg {
     static constexpr int BP = MODE == GM_RDX ? 2 : 1;
     static constexpr int OPS = (AP + BP) * GG_PLANE;
     static constexpr int STAGES = MODE == GM_WGRAD ? 6 : 3;
-    static constexpr int ACC_STEPS = MODE == GM_WGRAD ? 8 : MODE == GM_RDW ? 4 : 16;
+    static constexpr int ACC_STEPS = MODE == GM_WGRAD ? 16 : MODE == GM_RDW ? 4 : 16;
     // rows per chunk of a split tile (a result of GM_RDX has at most 16 stages and is not split)
     static constexpr int CHUNK_STEPS = MODE == GM_WGRAD ? 16 : MODE == GM_RDW ? 8 : 16;
 };
@@ -75,9 +75,10 @@ struct GradCfg {
 template <int MODE>
 struct GradShared {
     uint8_t ops[GradCfg<MODE>::STAGES][GradCfg<MODE>::OPS];      // 1024-byte aligned
-    uint64_t landed[GradCfg<MODE>::STAGES];      // TMA bytes of this CTA
-    uint64_t tail[GradCfg<MODE>::STAGES];        // its rows behind the group are cleared
-    uint64_t peer[GradCfg<MODE>::STAGES];        // leader: the other CTA's operands are in place
+    uint8_t out[GG_EPI_WARPS][GG_OUT];               // epilogue: 32 rows of 128 bytes per warp
+    uint64_t landed[GradCfg<MODE>::STAGES];          // leader: TMA bytes of both CTAs
+    uint64_t tail[GradCfg<MODE>::STAGES];            // its rows behind the group are cleared
+    uint64_t peer[GradCfg<MODE>::STAGES];            // leader: those of the other CTA are
     uint64_t empty[GradCfg<MODE>::STAGES];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
@@ -92,8 +93,7 @@ struct GradArgs {
     int R;                     // contraction rows of all groups
     int M, N, G;               // C is [G, M, N]
     int MT, NT, tiles, full, chunk_steps;
-    float* c;
-    __nv_bfloat16* cb;         // GM_RDX
+    float* c;                  // (GM_RDX stores through its map alone)
     int accumulate;
     float* part;               // [pairs][2][256][256]
     int32_t* flag;
@@ -137,12 +137,24 @@ __device__ __forceinline__ void gg_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// (cta_group::2: the barrier may be the other CTA's)
 __device__ __forceinline__ void gg_tma(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst),
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+template <bool ADD>
+__device__ __forceinline__ void gg_tma_store(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+    if (ADD)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                     "r"(x), "r"(y), "r"(z), "r"(src)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                     "r"(x), "r"(y), "r"(z), "r"(src)
+                     : "memory");
 }
 template <int REGS>
 __device__ __forceinline__ void gg_regs_down() {
@@ -157,11 +169,10 @@ __device__ __forceinline__ void gg_st16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
-// 16 lanes x 32 columns: lane t holds, for j = 0..3, r[4j], r[4j+1] = row t/4,
-// columns 8j + 2(t%4) + {0, 1}, and r[4j+2], r[4j+3] = row 8 + t/4.
-__device__ __forceinline__ void gg_ld16x32(uint32_t taddr, uint32_t (&r)[16]) {
+// 32 lanes x 16 columns: lane = row.
+__device__ __forceinline__ void gg_ld32x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
@@ -280,7 +291,9 @@ struct Steps {
 // ---- the kernel ----------------------------------------------------------------------
 template <int MODE>
 __global__ void __launch_bounds__(GG_THREADS, 1)
-    k_grad_gemm(const __grid_constant__ GradArgs a, const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map) {
+    k_grad_gemm(const __grid_constant__ GradArgs a, const __grid_constant__ CUtensorMap a_map,
+                const __grid_constant__ CUtensorMap b_map, const __grid_constant__ CUtensorMap c_map,
+                const __grid_constant__ CUtensorMap part_map) {
     pdl_begin();
     using Cfg = GradCfg<MODE>;
     constexpr int AP = Cfg::AP, BP = Cfg::BP, STAGES = Cfg::STAGES;
@@ -295,7 +308,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sh.landed[s]), 1);
             mbar_init(smem_u32(&sh.tail[s]), GG_TAIL_WARPS);
-            mbar_init(smem_u32(&sh.peer[s]), 1);
+            mbar_init(smem_u32(&sh.peer[s]), GG_TAIL_WARPS);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -366,34 +379,45 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
 
     // Stages with rows behind their group's last one (the last stage of a group
     // with another row count than a multiple of 64): dy and x of other rows have
-    // landed there and are cleared (rows behind R read as 0).  tails: parity of each stage's next clearing.
+    // landed there and are cleared (rows behind R read as 0).  Each CTA then
+    // counts its own bytes.  tails: parity of each stage's next clearing.
     uint32_t tails = 0;
     auto has_tail = [&](const Segment& s, int st) {
         return MODE == GM_WGRAD && s.r1 < a.R && s.r1 - s.r0 - st * GG_K < GG_K;
     };
-    auto wait_tail = [&](const Segment& s, int st) {
-        if (!has_tail(s, st)) return true;
+    auto tail_parity = [&]() {
         const uint32_t p = tails >> stage & 1u;
         tails ^= 1u << stage;
-        return wait(smem_u32(&sh.tail[stage]), p);
+        return p;
     };
 
     if (warp < GG_TAIL_WARP0) {
         gg_regs_down<GG_REGS_LOAD>();
         if (warp == 0 && lane == 0) {
-            // ---------------- bf16 operands by TMA ----------------
-            uint32_t filled = 0, parity = 0;      // bit s: stage s has a copy, and its phase
+            // ---------------- operands by TMA ----------------
+            // The bytes of both CTAs are counted on the leader's barrier.  (The
+            // waits here run to their limit even when another role has given
+            // up: "empty" reaches both CTAs, so both have then issued the same
+            // stages, and the leader's last waits cover the copies of both.)
+            uint32_t filled = 0, parity = 0;      // bit s: this CTA's barrier of stage s is armed, and its phase
             constexpr uint32_t bytes = (AP + BP) * GG_PLANE;
             for (Steps s(walk0); s.on; s.advance()) {
-                if (*abort || !wait(smem_u32(&sh.empty[stage]), phase ^ 1u)) {
+                if (!mbar_wait_for<false>(smem_u32(&sh.empty[stage]), phase ^ 1u, a.wait_ns, nullptr)) {
                     give_up();
                     break;
                 }
-                const uint32_t bar = smem_u32(&sh.landed[stage]);
+                const bool tail = has_tail(s.seg, s.st);
+                const uint32_t own = smem_u32(&sh.landed[stage]);
+                const uint32_t bar = rank == 0 || tail ? own : gg_peer(own, 0);
                 uint32_t dst = smem_u32(sh.ops[stage]);
                 const int r = s.seg.r0 + s.st * GG_K;
                 const int m = s.seg.m0 + GG_HALF * (int)rank, n = s.seg.n0 + GG_HALF * (int)rank;
-                mbar_expect_tx(bar, bytes);
+                if (rank == 0 || tail) {
+                    const uint32_t p = rank == 0 ? phase : tail_parity();
+                    mbar_expect_tx(own, tail ? bytes : 2 * bytes);
+                    filled |= 1u << stage;
+                    parity = (parity & ~(1u << stage)) | (p << stage);
+                }
 #pragma unroll
                 for (int p = 0; p < AP; ++p, dst += GG_PLANE) {
                     if (MODE == GM_RDX) {
@@ -408,8 +432,6 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                     gg_tma(dst, &b_map, n, r, p, bar);
                     gg_tma(dst + GG_BLOCK, &b_map, n + 64, r, p, bar);
                 }
-                filled |= 1u << stage;
-                parity = (parity & ~(1u << stage)) | (phase << stage);
                 next_stage();
             }
             for (int s = 0; s < STAGES; ++s)
@@ -434,8 +456,12 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                         tc_fence_after();
                         const uint32_t d = tmem + buf * GG_TILE;
                         for (int s = st; s < st1; ++s) {
-                            if (!wait(smem_u32(&sh.landed[stage]), phase) || !wait_tail(seg, s) ||
-                                !wait(smem_u32(&sh.peer[stage]), phase)) {
+                            bool in = wait(smem_u32(&sh.landed[stage]), phase);
+                            if (in && has_tail(seg, s)) {
+                                const uint32_t p = tail_parity();
+                                in = wait(smem_u32(&sh.tail[stage]), p) && wait(smem_u32(&sh.peer[stage]), p);
+                            }
+                            if (!in) {
                                 give_up();
                                 ok = false;
                                 break;
@@ -483,36 +509,35 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                 const int v = __ldg(a.perm + i);
                 checked_index(v < 0 ? v : v / a.k_div, a.xrows, a.flag);
             }
-        } else if (warp == 3 && lane == 0 && rank == 1) {
-            // ---------------- "in place" to the leader ----------------
-            for (Steps s(walk0); s.on; s.advance()) {
-                if (!wait(smem_u32(&sh.landed[stage]), phase) || !wait_tail(s.seg, s.st)) {
-                    give_up();
-                    break;
-                }
-                gg_arrive(smem_u32(&sh.peer[stage]), 0);
-                next_stage();
-            }
         }
         __syncwarp();
     } else if (warp < GG_EPI_WARP0) {
         gg_regs_down<GG_REGS_LOAD>();
         if (MODE == GM_WGRAD && a.offsets) {
             // ---------------- rows behind a group's last one ----------------
+            // The leader's barriers pass every stage, the other CTA's only these.
             const int t = threadIdx.x - 32 * GG_TAIL_WARP0;
             for (Steps s(walk0); s.on; s.advance()) {
-                if (!warp_wait(smem_u32(&sh.landed[stage]), phase)) {
-                    give_up();
-                    break;
+                const bool tail = has_tail(s.seg, s.st);
+                if (rank == 0 || tail) {
+                    if (!warp_wait(smem_u32(&sh.landed[stage]), rank == 0 ? phase : tail_parity())) {
+                        give_up();
+                        break;
+                    }
                 }
-                if (has_tail(s.seg, s.st)) {
+                if (tail) {
                     const int valid = s.seg.r1 - s.seg.r0 - s.st * GG_K;
                     const uint32_t dst = smem_u32(sh.ops[stage]);
                     for (int i = t; i < Cfg::OPS / 16; i += 32 * GG_TAIL_WARPS)
                         if ((i >> 3 & (GG_K - 1)) >= valid) gg_st16(dst + i * 16, make_uint4(0u, 0u, 0u, 0u));
                     gg_fence_async();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.tail[stage]));
+                    if (lane == 0) {
+                        if (rank == 0)
+                            mbar_arrive(smem_u32(&sh.tail[stage]));
+                        else
+                            gg_arrive(smem_u32(&sh.peer[stage]), 0);
+                    }
                 }
                 next_stage();
             }
@@ -521,18 +546,22 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     } else {
         gg_regs_up<GG_REGS_EPI>();
         // ---------------- epilogue ----------------
-        // Warp (q, half): TMEM lanes 32 q .. + 31, columns 128 half .. + 127.
-        // acc[32 L + 4 jj + 2 hh + e]... see gg_ld16x32: row 32 q + 16 L + 8 hh + t / 4.
-        const int q = warp & 3, half = (warp - GG_EPI_WARP0) >> 2, t4 = lane >> 2, c2 = 2 * (lane & 3);
+        // Warp (q, half): TMEM lanes 32 q .. + 31 (lane = row), columns 128 half
+        // .. + 127, 16 at a time into the sums.  Results leave through 32 rows x
+        // 128 bytes of shared memory (128-byte swizzle: 16-byte stores without
+        // bank conflicts) and TMA, which writes whole lines and cuts off what
+        // lies outside C; adding to C is its reduction.
+        const int q = warp & 3, half = (warp - GG_EPI_WARP0) >> 2;
+        const uint32_t out = smem_u32(sh.out[warp - GG_EPI_WARP0]);
         int buf = 0;
         uint32_t use = 0;
         Walk walk(walk0);
         Segment seg;
         bool ok = true;
         while (ok && walk.next(seg)) {
-            float acc[2][4][16];       // 16-row half, 32-column group, value
+            float acc[8][16];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i >> 6][(i >> 4) & 3][i & 15] = 0.0f;
+            for (int i = 0; i < 128; ++i) acc[i >> 4][i & 15] = 0.0f;
             for (int st = seg.s0; st < seg.s1; st += Cfg::ACC_STEPS) {
                 if (!warp_wait(smem_u32(&sh.acc_full[buf]), use >> buf & 1u)) {
                     give_up();
@@ -543,11 +572,10 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     uint32_t v[16];
-                    gg_ld16x32(tmem + ((uint32_t)(32 * q + 16 * (i >> 2)) << 16) + buf * GG_TILE + 128 * half + 32 * (i & 3), v);
+                    gg_ld32x16(tmem + ((uint32_t)(32 * q) << 16) + buf * GG_TILE + 128 * half + 16 * i, v);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        acc[i >> 2][i & 3][e] = __fadd_rn(acc[i >> 2][i & 3][e], __uint_as_float(v[e]));
+                    for (int e = 0; e < 16; ++e) acc[i][e] = __fadd_rn(acc[i][e], __uint_as_float(v[e]));
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -557,53 +585,45 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             }
             if (!ok) break;
             const bool whole = seg.slot < 0;
-            const int row0 = GG_HALF * (int)rank + 32 * q + t4, col0 = 128 * half;
-            if constexpr (MODE == GM_RDX) {
-                const int mlim = a.M - seg.m0, nlim = a.N - seg.n0;
+            const int mr = GG_HALF * (int)rank + 32 * q, nc = 128 * half;
+            constexpr int COLS = MODE == GM_RDX ? 64 : 32;      // of C per 128 bytes
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int m = row0 + 8 * k;
-                    __nv_bfloat16* o = a.cb + (size_t)(seg.m0 + m) * a.N + seg.n0;
+            for (int g = 0; g < 128 / COLS; ++g) {
+                // the previous 32 x 128 bytes have been read
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        // 16 columns of a row lie in 4 lanes, 2 in each of two groups of 8:
-                        // exchanged so that a lane stores 4 neighbours
-                        const float* r = &acc[k >> 1][j >> 1][8 * (j & 1) + 2 * (k & 1)];
-                        const uint32_t pe = bf16x2_rn(r[0], r[1]), po = bf16x2_rn(r[4], r[5]);
-                        const int src = (lane & ~3) + 2 * (lane & 1);
-                        const uint32_t e0 = __shfl_sync(0xffffffffu, pe, src), e1 = __shfl_sync(0xffffffffu, pe, src + 1);
-                        const uint32_t o0 = __shfl_sync(0xffffffffu, po, src), o1 = __shfl_sync(0xffffffffu, po, src + 1);
-                        const int col = col0 + 16 * j + 4 * (lane & 3);
-                        if (m < mlim && col < nlim)
-                            *reinterpret_cast<uint2*>(o + col) = (lane & 2) ? make_uint2(o0, o1) : make_uint2(e0, e1);
+                for (int j = 0; j < 8; ++j) {
+                    uint4 v;
+                    if constexpr (MODE == GM_RDX) {
+                        const float* r = &acc[4 * g + (j >> 1)][8 * (j & 1)];
+                        v = make_uint4(bf16x2_rn(r[0], r[1]), bf16x2_rn(r[2], r[3]), bf16x2_rn(r[4], r[5]),
+                                       bf16x2_rn(r[6], r[7]));
+                    } else {
+                        const float* r = &acc[2 * g + (j >> 2)][4 * (j & 3)];
+                        v = make_uint4(__float_as_uint(r[0]), __float_as_uint(r[1]), __float_as_uint(r[2]),
+                                       __float_as_uint(r[3]));
                     }
+                    gg_st16(out + gg_swz(lane, j), v);
                 }
-            } else {
-                float* out = whole ? a.c + ((size_t)seg.g * a.M + seg.m0) * a.N + seg.n0
-                                   : a.part + (size_t)seg.slot * (GG_TILE * GG_TILE);
-                const size_t ld = whole ? a.N : GG_TILE;
-                const int mlim = whole ? a.M - seg.m0 : GG_TILE, nlim = whole ? a.N - seg.n0 : GG_TILE;
-                const bool add = whole && a.accumulate;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int m = row0 + 8 * k;
-                    if (m >= mlim) continue;
-                    float* o = out + (size_t)m * ld + col0 + c2;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (col0 + 8 * j >= nlim) break;
-                        const float* r = &acc[k >> 1][j >> 2][4 * (j & 3) + 2 * (k & 1)];
-                        float2 w = make_float2(r[0], r[1]);
-                        if (add) {
-                            const float2 b = *reinterpret_cast<const float2*>(o + 8 * j);
-                            w.x = __fadd_rn(b.x, w.x);
-                            w.y = __fadd_rn(b.y, w.y);
-                        }
-                        *reinterpret_cast<float2*>(o + 8 * j) = w;
+                gg_fence_async();
+                __syncwarp();
+                if (lane == 0) {
+                    const int n = nc + COLS * g;
+                    if (!whole)
+                        gg_tma_store<false>(&part_map, n, mr, seg.slot, out);
+                    else if (seg.m0 + mr < a.M && seg.n0 + n < a.N) {
+                        if (MODE != GM_RDX && a.accumulate)
+                            gg_tma_store<true>(&c_map, seg.n0 + n, seg.m0 + mr, seg.g, out);
+                        else
+                            gg_tma_store<false>(&c_map, seg.n0 + n, seg.m0 + mr, seg.g, out);
                     }
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
 
     tc_fence_before();
@@ -888,8 +908,44 @@ static int grad_grid() {
     });
 }
 
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Tensor map of `planes` row-major matrices [rows, cols] (rows ld elements
+// apart, matrices one behind the other): boxes of 128 bytes x box_rows with the
+// 128-byte swizzle.  What lies outside reads as 0 and is not written.
+static cudaError_t grad_map(const void* p, CUtensorMapDataType type, long long ld, int rows, int cols, int planes,
+                            int box_cols, int box_rows, CUtensorMap* map) {
+    static const EncodeTiled encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t row = (cuuint64_t)ld * (128 / box_cols);
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {row, row * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+    return encode(map, type, 3, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+static cudaError_t bf16_map(const void* p, long long ld, int rows, int cols, int planes, int box_rows,
+                            CUtensorMap* map) {
+    return grad_map(p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ld, rows, cols, planes, 64, box_rows, map);
+}
+
 template <int MODE>
-static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUtensorMap& b_map, cudaStream_t st) {
+static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUtensorMap& b_map, void* c,
+                               cudaStream_t st) {
     const int grid = grad_grid<MODE>();
     if (grid <= 0) return cudaErrorInvalidConfiguration;
     const int pairs = grid / 2;
@@ -900,6 +956,19 @@ static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUten
     a.tiles = (int)tiles;
     a.full = a.tiles / pairs * pairs;
     a.chunk_steps = GradCfg<MODE>::CHUNK_STEPS;
+    const int rem = a.tiles - a.full;
+    const bool split = rem > 0 && a.R > a.chunk_steps * GG_K;
+    CUtensorMap c_map, part_map;
+    cudaError_t e;
+    if (MODE == GM_RDX)
+        e = grad_map(c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.N, a.M, a.N, 1, 64, 32, &c_map);
+    else
+        e = grad_map(c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.N, a.M, a.N, a.G, 32, 32, &c_map);
+    part_map = c_map;
+    if (e == cudaSuccess && split)
+        e = grad_map(a.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, GG_TILE, GG_TILE, GG_TILE, 2 * pairs, 32, 32, &part_map);
+    if (e != cudaSuccess) return e;
+    a.c = (float*)c;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(GG_THREADS);
@@ -914,47 +983,12 @@ static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUten
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k_grad_gemm<MODE>, a, a_map, b_map);
+    e = cudaLaunchKernelEx(&cfg, k_grad_gemm<MODE>, a, a_map, b_map, c_map, part_map);
     count_launches(1);
-    const int rem = a.tiles - a.full;
-    if (e != cudaSuccess || rem == 0 || a.R <= a.chunk_steps * GG_K) return e;
+    if (e != cudaSuccess || !split) return e;
     e = launch_pdl(k_grad_fixup, dim3((unsigned)rem, GG_TILE / 8), dim3(256), 0, st, a, pairs);
     count_launches(1);
     return e;
-}
-
-typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-static EncodeTiled encode_tiled() {
-    static const EncodeTiled encode = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            f = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(f);
-    }();
-    return encode;
-}
-
-// Tensor map of `planes` row-major bf16 matrices [rows, cols] (rows ld apart,
-// matrices one behind the other): boxes of 64 columns with the 128-byte
-// swizzle; what lies outside reads as 0.
-static cudaError_t bf16_map(const void* p, long long ld, int rows, int cols, int planes, int box_rows,
-                            CUtensorMap* map) {
-    const EncodeTiled encode = encode_tiled();
-    if (!encode) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
 }
 
 // Workspace: the error word (256 bytes), the operands as bf16, the parts of
@@ -1018,12 +1052,11 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
     a.M = N;
     a.N = K;
     a.G = G;
-    a.c = dw;
     a.accumulate = accumulate;
     a.part = (float*)((char*)ws + wgrad_part_offset(R, K));
     a.flag = flag;
     a.wait_ns = wait_ns;
-    return launch_grad<GM_WGRAD>(a, a_map, b_map, st);
+    return launch_grad<GM_WGRAD>(a, a_map, b_map, dw, st);
 }
 
 cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t* codes, const uint8_t* scales,
@@ -1076,10 +1109,9 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
         GradArgs d = a;
         d.R = T;
         d.M = E;
-        d.c = dw;
         d.accumulate = accumulate;
         d.part = (float*)(b + L.part);
-        e = launch_grad<GM_RDW>(d, a_map, b_map, st);
+        e = launch_grad<GM_RDW>(d, a_map, b_map, dw, st);
     }
     if (e == cudaSuccess && dx) {
         e = bf16_map(s.dlp, Ep, T, Ep, 2, GG_HALF, &a_map);
@@ -1087,8 +1119,7 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
         if (e != cudaSuccess) return e;
         a.R = E;
         a.M = T;
-        a.cb = (__nv_bfloat16*)dx;
-        e = launch_grad<GM_RDX>(a, a_map, b_map, st);
+        e = launch_grad<GM_RDX>(a, a_map, b_map, dx, st);
     }
     if (e == cudaSuccess && db) {
         e = launch_pdl(k_router_bias, dim3((unsigned)((E + 31) / 32)), dim3(1024), 0, st, (const float*)s.bias_part,
