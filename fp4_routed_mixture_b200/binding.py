@@ -8,7 +8,6 @@ importing this module without the built library raises ImportError.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -415,14 +414,16 @@ def _arg(t, name: str, dtype, shape, dev, strided: bool = False):
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _bad(f"{name} must be a CUDA tensor")
-    if t.device != dev:
-        _bad(f"{name} is on {t.device}, the call runs on {dev}")
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         _bad(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         _bad(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if not t.is_contiguous() and not (strided and t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
         _bad(f"{name} must be contiguous" + (" in its rows" if strided else ""))
+    if t.device != dev:
+        _bad(f"{name} is on {t.device}, the call runs on {dev}")
     return t.data_ptr()
 
 
@@ -438,42 +439,55 @@ def _matrix(t, name: str):
     return t.shape
 
 
+def _table(t, name: str) -> int:
+    """Groups a table of offsets bounds (its length less one)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.numel() < 2:
+        _bad(f"{name} must be a 1-D tensor of at least two entries")
+    return t.numel() - 1
+
+
 def _mask_arg(t, T, dev):
-    if t is not None and isinstance(t, torch.Tensor) and t.dtype == torch.bool:
+    if t is not None and isinstance(t, torch.Tensor) and t.dtype is torch.bool:
         t = t.view(torch.uint8)
     return _arg(t, "token_mask", torch.uint8, (T,), dev)
 
 
-def _ws_arg(ws, nbytes: int, dev):
-    """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
-    if nbytes == 0:
-        raise MoeError(-2, "unsupported dims")
+def _new(shape, dtype, dev, stream):
+    """An output the call allocates: with a `stream` its memory belongs to that
+    stream (memory of the current one may still be in use there)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _ws_arg(ws, size, dims, dev, stream):
+    """(tensor, pointer, bytes) of the caller's workspace, or of a new one of
+    size(*dims) bytes."""
     if ws is None:
-        ws = _empty_aligned(nbytes, dev)
-    return ws, _arg(ws, "ws", torch.uint8, (ws.numel(),), dev), ws.numel()
-
-
-def _allocates(fn):
-    """With a `stream`, what the call allocates belongs to that stream (memory
-    of the current one may still be in use there)."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, stream=stream, **kw)
-    return call
+        nbytes = size(*dims)
+        if nbytes == 0:
+            raise MoeError(-2, "unsupported dims")
+        ws = _new((nbytes,), torch.uint8, dev, stream)
+    n = ws.numel() if isinstance(ws, torch.Tensor) else 0
+    return ws, _arg(ws, "ws", torch.uint8, (n,), dev), n
 
 
 def _call(dev, fn, args, stream):
     """fn(*args, stream) with the tensors' device current."""
-    if stream is not None and stream.device != dev:
-        _bad(f"stream is on {stream.device}, the tensors on {dev}")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)     # (current_stream(dev) takes 2 us)
+    else:
+        if stream.device != dev:
+            _bad(f"stream is on {stream.device}, the tensors on {dev}")
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, _stream(stream)))
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
+            status = fn(*args, handle)
+    if status != MOE_OK:
+        _check(status)
 
 
 def moe_balance_workspace_bytes(T_max: int, E: int, S_max: int = 1) -> int:
@@ -483,7 +497,6 @@ def moe_balance_workspace_bytes(T_max: int, E: int, S_max: int = 1) -> int:
     return n
 
 
-@_allocates
 def moe_balance_loss(logits, topk_idx, coef: float, seq_offsets=None, token_mask=None, ws=None, out=None,
                      stream=None):
     """logits [T,E] fp32, topk_idx [T,k] int32, seq_offsets [S+1] int32 or None
@@ -493,23 +506,22 @@ def moe_balance_loss(logits, topk_idx, coef: float, seq_offsets=None, token_mask
     T, E = _matrix(logits, "logits")
     k = _matrix(topk_idx, "topk_idx")[1]
     dev = logits.device
-    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    S = 1 if seq_offsets is None else _table(seq_offsets, "seq_offsets")
     if out is None:
-        out = (torch.empty(1, dtype=torch.float32, device=dev),
-               torch.empty((max(S, 0), E), dtype=torch.int32, device=dev),
-               torch.empty((max(S, 0), E), dtype=torch.float32, device=dev),
-               torch.empty(max(S, 0) + 1, dtype=torch.int32, device=dev))
+        out = (_new(1, torch.float32, dev, stream),
+               _new((S, E), torch.int32, dev, stream),
+               _new((S, E), torch.float32, dev, stream),
+               _new(S + 1, torch.int32, dev, stream))
     loss, counts, mean_prob, tokens = out
     p = (_arg(logits, "logits", torch.float32, (T, E), dev), _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
          _arg(seq_offsets, "seq_offsets", torch.int32, (S + 1,), dev), _mask_arg(token_mask, T, dev))
     o = (_arg(counts, "counts", torch.int32, (S, E), dev), _arg(mean_prob, "mean_prob", torch.float32, (S, E), dev),
          _arg(tokens, "tokens", torch.int32, (S + 1,), dev), _arg(loss, "loss", torch.float32, (1,), dev))
-    ws, pw, nw = _ws_arg(ws, lib.moe_balance_workspace_bytes(T, E, S), dev)
+    ws, pw, nw = _ws_arg(ws, lib.moe_balance_workspace_bytes, (T, E, S), dev, stream)
     _call(dev, lib.moe_balance_loss, (*p, T, E, k, S, coef, *o, pw, nw), stream)
     return out
 
 
-@_allocates
 def moe_route_backward(logits, topk_idx, gates=None, dgates=None, dloss=None, coef: float = 0.0, counts=None,
                        tokens=None, seq_offsets=None, token_mask=None, ws=None, out=None, stream=None):
     """Gradient of the logits [T,E] fp32 from the gates' gradient dgates [T,k]
@@ -519,9 +531,9 @@ def moe_route_backward(logits, topk_idx, gates=None, dgates=None, dloss=None, co
     T, E = _matrix(logits, "logits")
     k = _matrix(topk_idx, "topk_idx")[1]
     dev = logits.device
-    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    S = 1 if seq_offsets is None else _table(seq_offsets, "seq_offsets")
     if out is None:
-        out = torch.empty((T, E), dtype=torch.float32, device=dev)
+        out = _new((T, E), torch.float32, dev, stream)
     if ws is not None and ws.numel() < 4:
         _bad("ws must hold at least 4 bytes")
     p = (_arg(logits, "logits", torch.float32, (T, E), dev), _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
@@ -542,7 +554,6 @@ def moe_router_backward_workspace_bytes(T_max: int, H: int, E: int) -> int:
     return n
 
 
-@_allocates
 def moe_router_logits_backward(dlogits, w_router, x=None, codes=None, scales=None, accumulate: bool = False, ws=None,
                                out=None, stream=None):
     """dlogits [T,E] fp32, w_router [E,H] fp32, and x [T,H] bf16 or its 8-bit
@@ -555,28 +566,27 @@ def moe_router_logits_backward(dlogits, w_router, x=None, codes=None, scales=Non
     if out is None:
         if accumulate:
             _bad("accumulate needs out")
-        out = (torch.empty((T, H), dtype=torch.bfloat16, device=dev),
-               torch.empty((E, H), dtype=torch.float32, device=dev),
-               torch.empty(E, dtype=torch.float32, device=dev))
+        out = (_new((T, H), torch.bfloat16, dev, stream),
+               _new((E, H), torch.float32, dev, stream),
+               _new(E, torch.float32, dev, stream))
     dx, dw, db = out
     p = (_arg(dlogits, "dlogits", torch.float32, (T, E), dev), _arg(x, "x", torch.bfloat16, (T, H), dev),
          _arg(codes, "codes", torch.uint8, (T, H), dev), _arg(scales, "scales", torch.uint8, (T, H // 128), dev),
          _arg(w_router, "w_router", torch.float32, (E, H), dev))
     o = (_arg(dx, "dx", torch.bfloat16, (T, H), dev), _arg(dw, "dw", torch.float32, (E, H), dev),
          _arg(db, "dbias", torch.float32, (E,), dev))
-    ws, pw, nw = _ws_arg(ws, lib.moe_router_backward_workspace_bytes(T, H, E), dev)
+    ws, pw, nw = _ws_arg(ws, lib.moe_router_backward_workspace_bytes, (T, H, E), dev, stream)
     _call(dev, lib.moe_router_logits_backward, (*p, T, H, E, *o, int(accumulate), pw, nw), stream)
     return out
 
 
-@_allocates
 def moe_ckpt_pack(x, out=None, stream=None):
     """x [T,K] bf16 (rows may be strided) -> (codes [T,K], scales [T,K/128]) uint8."""
     T, K = _matrix(x, "x")
     dev = x.device
     if out is None:
-        out = (torch.empty((T, K), dtype=torch.uint8, device=dev),
-               torch.empty((T, K // 128), dtype=torch.uint8, device=dev))
+        out = (_new((T, K), torch.uint8, dev, stream),
+               _new((T, K // 128), torch.uint8, dev, stream))
     codes, scales = out
     px = _arg(x, "x", torch.bfloat16, (T, K), dev, strided=True)
     o = (_arg(codes, "codes", torch.uint8, (T, K), dev), _arg(scales, "scales", torch.uint8, (T, K // 128), dev))
@@ -584,28 +594,26 @@ def moe_ckpt_pack(x, out=None, stream=None):
     return out
 
 
-@_allocates
 def moe_ckpt_unpack(codes, scales, out=None, stream=None):
     """The activation a checkpoint holds, [T,K] bf16 (`out`'s rows may be strided)."""
     T, K = _matrix(codes, "codes")
     dev = codes.device
     if out is None:
-        out = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        out = _new((T, K), torch.bfloat16, dev, stream)
     p = (_arg(codes, "codes", torch.uint8, (T, K), dev), _arg(scales, "scales", torch.uint8, (T, K // 128), dev))
     po = _arg(out, "out", torch.bfloat16, (T, K), dev, strided=True)
     _call(dev, lib.moe_ckpt_unpack, (*p, T, K, po, _row_stride(out)), stream)
     return out
 
 
-@_allocates
 def moe_ckpt_swiglu_backward(gu_codes, gu_scales, dh, need_h: bool = False, out=None, stream=None):
     """Checkpoint of the gate|up activations [T,2I], dh [T,I] bf16 (rows may be
     strided) -> (dgu [T,2I] bf16, h [T,I] bf16 or None)."""
     T, I = _matrix(dh, "dh")
     dev = dh.device
     if out is None:
-        out = (torch.empty((T, 2 * I), dtype=torch.bfloat16, device=dev),
-               torch.empty((T, I), dtype=torch.bfloat16, device=dev) if need_h else None)
+        out = (_new((T, 2 * I), torch.bfloat16, dev, stream),
+               _new((T, I), torch.bfloat16, dev, stream) if need_h else None)
     dgu, h = out
     if need_h and h is None:
         _bad("out holds no tensor for h")
@@ -625,7 +633,6 @@ def moe_ckpt_wgrad_workspace_bytes(R_max: int, N: int, K: int, G: int = 1) -> in
     return n
 
 
-@_allocates
 def moe_ckpt_wgrad(dy, codes, scales, offsets=None, perm=None, k: int = 1, dw=None, accumulate: bool = False, ws=None,
                    stream=None):
     """dy [R,N] bf16 (rows may be strided) and a checkpoint of x [X,K] -> the
@@ -634,17 +641,17 @@ def moe_ckpt_wgrad(dy, codes, scales, offsets=None, perm=None, k: int = 1, dw=No
     R, N = _matrix(dy, "dy")
     X, K = _matrix(codes, "codes")
     dev = dy.device
-    G = 1 if offsets is None else offsets.numel() - 1
+    G = 1 if offsets is None else _table(offsets, "offsets")
     shape = (N, K) if offsets is None else (G, N, K)
     if dw is None:
         if accumulate:
             _bad("accumulate needs dw")
-        dw = torch.empty(tuple(max(0, n) for n in shape), dtype=torch.float32, device=dev)
+        dw = _new(shape, torch.float32, dev, stream)
     p = (_arg(dy, "dy", torch.bfloat16, (R, N), dev, strided=True), _row_stride(dy),
          _arg(codes, "codes", torch.uint8, (X, K), dev), _arg(scales, "scales", torch.uint8, (X, K // 128), dev),
          _arg(offsets, "offsets", torch.int32, (G + 1,), dev), _arg(perm, "perm", torch.int32, (R,), dev))
     pd = _arg(dw, "dw", torch.float32, shape, dev)
-    ws, pw, nw = _ws_arg(ws, lib.moe_ckpt_wgrad_workspace_bytes(R, N, K, G), dev)
+    ws, pw, nw = _ws_arg(ws, lib.moe_ckpt_wgrad_workspace_bytes, (R, N, K, G), dev, stream)
     _call(dev, lib.moe_ckpt_wgrad, (*p, k, R, X, N, K, G, pd, int(accumulate), pw, nw), stream)
     return dw
 

@@ -29,9 +29,12 @@
 //   warps 4-7     GM_WGRAD: clear the rows behind a group's last one
 //   warps 8-15    epilogue, from two 256-column accumulators in TMEM
 // Work: pair p takes the tiles p, p + P, ... of the first floor(tiles / P) P
-// ones whole; the remaining tiles are cut into chunks of rows and dealt out
-// evenly, so that the last round is not left to a few pairs.  Parts of a tile
-// go to the workspace and k_grad_fixup adds them in a fixed order.
+// ones whole; the remaining tiles are cut so that the last round is not left to
+// a few pairs.  Where a tile has more rows than a chunk, its rows are cut into
+// chunks and dealt out evenly; the parts go to the workspace and k_grad_fixup
+// adds them in a fixed order.  Where it has fewer, storing C is what takes the
+// time (40 x 4096 x 4096: 2.6 us per tile and pair, the copy bandwidth): 2 or 4
+// pairs compute the same tile and store a part of its columns each.
 //
 // The tensor cores truncate when they add to the fp32 accumulator, always
 // towards zero: about 7e-9 of the result per MMA (measured: 1.2e-6 after 256
@@ -93,6 +96,7 @@ struct GradArgs {
     int R;                     // contraction rows of all groups
     int M, N, G;               // C is [G, M, N]
     int MT, NT, tiles, full, chunk_steps;
+    int ways;                  // pairs per remaining tile (1: cut by rows)
     float* c;                  // (GM_RDX stores through its map alone)
     int accumulate;
     float* part;               // [pairs][2][256][256]
@@ -215,6 +219,7 @@ struct Segment {
     int r0, r1;         // contraction rows of its group
     int s0, s1;         // stages
     int slot;           // -1: the whole tile, else the part's place
+    int c0, c1;         // columns of the tile to store
 };
 
 // Walks a pair's segments; every role walks the same ones.
@@ -226,16 +231,24 @@ struct Walk {
     __device__ Walk(const GradArgs& a, const int32_t* pre, int p, int P)
         : args(&a), rem_pre(pre), pair(p), pairs(P), next_full(p), first_part(true) {
         const int rem = a.tiles - a.full;
-        const long long W = rem > 0 ? pre[rem] : 0;
+        const long long W = rem > 0 && a.ways == 1 ? pre[rem] : 0;
         chunk = (int)(W * p / P);
         chunk_end = (int)(W * (p + 1) / P);
     }
     __device__ bool next(Segment& s) {
         const GradArgs& a = *args;
         int t;
+        s.c0 = 0;
+        s.c1 = GG_TILE;
         if (next_full < a.full) {
             t = next_full;
             next_full += pairs;
+        } else if (a.ways > 1) {
+            if (!first_part || pair >= (a.tiles - a.full) * a.ways) return false;
+            first_part = false;
+            t = a.full + pair / a.ways;
+            s.c0 = (GG_TILE / a.ways) * (pair % a.ways);
+            s.c1 = s.c0 + GG_TILE / a.ways;
         } else if (chunk < chunk_end) {
             int lo = 0, hi = a.tiles - a.full - 1;        // last tile with rem_pre <= chunk
             while (lo < hi) {
@@ -255,7 +268,7 @@ struct Walk {
         s.s0 = 0;
         s.s1 = steps;
         s.slot = -1;
-        if (t >= a.full) {
+        if (t >= a.full && a.ways == 1) {
             const int b = rem_pre[t - a.full], e = rem_pre[t - a.full + 1];
             const int c1 = min(chunk_end, e);
             if (chunk > b || c1 < e) {
@@ -294,7 +307,6 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     k_grad_gemm(const __grid_constant__ GradArgs a, const __grid_constant__ CUtensorMap a_map,
                 const __grid_constant__ CUtensorMap b_map, const __grid_constant__ CUtensorMap c_map,
                 const __grid_constant__ CUtensorMap part_map) {
-    pdl_begin();
     using Cfg = GradCfg<MODE>;
     constexpr int AP = Cfg::AP, BP = Cfg::BP, STAGES = Cfg::STAGES;
     extern __shared__ uint8_t gg_raw_smem[];
@@ -319,27 +331,9 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 2) {
-        // chunks in front of each split tile (fewer than `pairs` tiles)
-        const int rem = a.tiles - a.full;
-        int run = 0;
-        for (int i0 = 0; i0 < rem; i0 += 32) {
-            int n = 0;
-            if (i0 + lane < rem) {
-                int r0, r1;
-                gg_rows(a, (a.full + i0 + lane) / (a.MT * a.NT), r0, r1);
-                n = (gg_steps(r1 - r0) + a.chunk_steps - 1) / a.chunk_steps;
-            }
-            int x = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            if (i0 + lane < rem) sh.rem_pre[i0 + lane] = run + x - n;
-            run += __shfl_sync(0xffffffffu, x, 31);
-        }
-        if (lane == 0) sh.rem_pre[rem] = run;
+    if (warp == 1 && lane < 4) {
+        const CUtensorMap* m = lane == 0 ? &a_map : lane == 1 ? &b_map : lane == 2 ? &c_map : &part_map;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem_base)),
@@ -352,6 +346,34 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     gg_cluster_sync();      // the peer's barriers exist before any remote arrive
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
+    // All of this needs nothing of the kernel in front; what follows does.  (Two
+    // of these blocks do not fit an SM: TMEM is free when one starts.)
+    pdl_begin();
+    if (a.ways == 1 && a.tiles > a.full) {
+        if (warp == 2) {
+            // chunks in front of each split tile (fewer than `pairs` tiles)
+            const int rem = a.tiles - a.full;
+            int run = 0;
+            for (int i0 = 0; i0 < rem; i0 += 32) {
+                int n = 0;
+                if (i0 + lane < rem) {
+                    int r0, r1;
+                    gg_rows(a, (a.full + i0 + lane) / (a.MT * a.NT), r0, r1);
+                    n = (gg_steps(r1 - r0) + a.chunk_steps - 1) / a.chunk_steps;
+                }
+                int x = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (i0 + lane < rem) sh.rem_pre[i0 + lane] = run + x - n;
+                run += __shfl_sync(0xffffffffu, x, 31);
+            }
+            if (lane == 0) sh.rem_pre[rem] = run;
+        }
+        __syncthreads();
+    }
     volatile int32_t* abort = &sh.abort;
     auto give_up = [&]() {
         *abort = 1;
@@ -589,6 +611,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             constexpr int COLS = MODE == GM_RDX ? 64 : 32;      // of C per 128 bytes
 #pragma unroll
             for (int g = 0; g < 128 / COLS; ++g) {
+                if (nc + COLS * g < seg.c0 || nc + COLS * g >= seg.c1) continue;
                 // the previous 32 x 128 bytes have been read
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
@@ -638,49 +661,51 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
 // tile, 8 rows of it).
 __global__ void __launch_bounds__(256) k_grad_fixup(GradArgs a, int pairs) {
     pdl_begin();
-    const int rem = a.tiles - a.full, i = blockIdx.x;
-    __shared__ int s_b, s_e, s_W;
+    const int rem = a.tiles - a.full, i = blockIdx.x, per = a.MT * a.NT;
+    __shared__ int s_slot[GG_MAX_PAIRS], s_n;
     if (threadIdx.x < 32) {
-        // chunks of all split tiles, and of those in front of tile i
-        int all = 0, before = 0, own = 0;
-        for (int j = threadIdx.x; j < rem; j += 32) {
+        // chunks of all split tiles, of those in front of tile i, and its own
+        const int lane = threadIdx.x;
+        int all = 0, b = 0, own = 0;
+        for (int j = lane; j < rem; j += 32) {
             int r0, r1;
-            gg_rows(a, (a.full + j) / (a.MT * a.NT), r0, r1);
+            gg_rows(a, (a.full + j) / per, r0, r1);
             const int n = (gg_steps(r1 - r0) + a.chunk_steps - 1) / a.chunk_steps;
             all += n;
-            before += j < i ? n : 0;
+            b += j < i ? n : 0;
             own += j == i ? n : 0;
         }
-        all = warp_sum(all);
-        before = warp_sum(before);
-        own = warp_sum(own);
-        if (threadIdx.x == 0) {
-            s_W = all;
-            s_b = before;
-            s_e = before + own;
+        const long long W = warp_sum(all);
+        b = warp_sum(b);
+        const int e = b + warp_sum(own);
+        // the pairs whose range of chunks meets the tile's, in order
+        int n = 0;
+        for (int p0 = 0; p0 < pairs; p0 += 32) {
+            const int p = p0 + lane, c0 = (int)(W * p / pairs), c1 = (int)(W * (p + 1) / pairs);
+            const bool in = p < pairs && c0 < c1 && c0 < e && c1 > b;
+            const uint32_t m = __ballot_sync(0xffffffffu, in);
+            // (it is a pair's second part where the pair's range begins in an earlier tile)
+            if (in) s_slot[n + __popc(m & ((1u << lane) - 1))] = 2 * p + (c0 < b ? 1 : 0);
+            n += __popc(m);
         }
+        if (lane == 0) s_n = n;
     }
     __syncthreads();
-    const long long W = s_W;
-    auto range0 = [&](int p) { return (int)(W * p / pairs); };
-    // first pair whose range reaches past the tile's first chunk
-    int p0 = (int)((long long)s_b * pairs / W);
-    while (p0 > 0 && range0(p0) > s_b) --p0;
-    while (range0(p0 + 1) <= s_b) ++p0;
-    if (range0(p0 + 1) >= s_e) return;        // one pair computed the whole tile
-    const int per = a.MT * a.NT, t = a.full + i, ti = t % per;
+    const int n = s_n;
+    if (n == 1) return;        // one pair computed the whole tile
+    const int t = a.full + i, ti = t % per;
     const int m0 = (ti / a.NT) * GG_TILE, n0 = (ti % a.NT) * GG_TILE;
     float* out = a.c + ((size_t)(t / per) * a.M + m0) * a.N + n0;
-    for (int e = threadIdx.x; e < 8 * (GG_TILE / 4); e += 256) {
-        const int m = blockIdx.y * 8 + e / (GG_TILE / 4), n = 4 * (e % (GG_TILE / 4));
-        if (m0 + m >= a.M || n0 + n >= a.N) continue;
-        float4* o = reinterpret_cast<float4*>(out + (size_t)m * a.N + n);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int m = blockIdx.y * 8 + (threadIdx.x >> 6) + 4 * h, c = 4 * (threadIdx.x & 63);
+        if (m0 + m >= a.M || n0 + c >= a.N) continue;
+        float4* o = reinterpret_cast<float4*>(out + (size_t)m * a.N + c);
+        const float* p = a.part + m * GG_TILE + c;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = p0; p < pairs && range0(p) < s_e; ++p) {
-            if (range0(p + 1) == range0(p)) continue;
-            // the tile is the pair's second part when its range begins in an earlier tile
-            const int slot = 2 * p + (range0(p) < s_b ? 1 : 0);
-            const float4 v = __ldg(reinterpret_cast<const float4*>(a.part + (size_t)slot * (GG_TILE * GG_TILE) + m * GG_TILE + n));
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p + (size_t)s_slot[j] * (GG_TILE * GG_TILE)));
             s.x = __fadd_rn(s.x, v.x);
             s.y = __fadd_rn(s.y, v.y);
             s.z = __fadd_rn(s.z, v.z);
@@ -832,8 +857,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_grad_prepare(PrepareArgs a) {
             long long src = i;
             if (i >= a.items) continue;
             if (a.perm) {
-                const int r = (int)(i / K8), v = __ldg(a.perm + r);
-                const int x = v < 0 ? 0 : v / a.k_div;
+                const int r = a.items >> 31 ? (int)(i / K8) : (int)((uint32_t)i / (uint32_t)K8);
+                const int v = __ldg(a.perm + r), x = v < 0 ? 0 : v / a.k_div;
                 src = (long long)(x < a.xrows ? x : 0) * K8 + (i - (long long)r * K8);    // (bad entries: row 0)
             }
             c[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + src * 8));
@@ -958,6 +983,8 @@ static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUten
     a.chunk_steps = GradCfg<MODE>::CHUNK_STEPS;
     const int rem = a.tiles - a.full;
     const bool split = rem > 0 && a.R > a.chunk_steps * GG_K;
+    // (4 ways: 64 columns, the narrowest store of GM_RDX)
+    a.ways = split || rem == 0 ? 1 : pairs >= 4 * rem ? 4 : pairs >= 2 * rem ? 2 : 1;
     CUtensorMap c_map, part_map;
     cudaError_t e;
     if (MODE == GM_RDX)
