@@ -20,9 +20,13 @@
 
 namespace moe {
 
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 512;             // k_balance_rows: 2 CTAs per SM
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kBalMaxChunks = 148 * 4;
+constexpr int kBalMaxChunks = 148 * 2;
+constexpr int kRedThreads = 256, kRedWarps = kRedThreads / 32;
+// Calls of at most this many rows and sequences run in one CTA and launch (8
+// rows of 256 logits: one launch of 3 us less).
+constexpr int kBalSingleT = 128, kBalSingleS = 64;
 
 struct BalanceWs {
     size_t meta, prob, hits, part, total;
@@ -67,6 +71,12 @@ struct SeqTable {
         }
         return lo;
     }
+    // sequence s does not ascend within [0, T]
+    __device__ bool bad(int s) const {
+        if (!off) return false;
+        const int b = __ldg(off + s), e = __ldg(off + s + 1);
+        return b < 0 || e > T || e < b;
+    }
 };
 
 // Column of a lane's value v: four neighbours per 128 columns (VEC, one
@@ -95,31 +105,34 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
     }
 }
 
-// x <- softmax of the row the warp holds (columns behind E hold -inf and get
-// 0).  A row of -inf alone has no distribution: its probabilities are 0.  The
-// exponent is taken after the maximum is subtracted, the sum is fp32.
+// 2^x, within 2 ulp; below 2^-126: 0.
+__device__ __forceinline__ float bal_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// x <- exp(x - max) of the row the warp holds (columns behind E hold -inf and
+// get 0); returns this lane's part of their sum.  NaN is the maximum where the
+// row has one, so such a row becomes NaN; +inf - +inf does the same.  A row of
+// -inf alone has no distribution: all 0.  The difference is taken before the
+// factor log2(e): two roundings of it, |x - max| 2^-24 each.
 template <int N>
-__device__ __forceinline__ void row_softmax(float (&x)[N]) {
+__device__ __forceinline__ float row_exp(float (&x)[N]) {
     float m = x[0];
-    bool nan = false;
 #pragma unroll
-    for (int v = 0; v < N; ++v) {
-        m = fmaxf(m, x[v]);
-        nan |= x[v] != x[v];
-    }
-    m = warp_max(m);
+    for (int v = 1; v < N; ++v) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(x[v]));
+    asm volatile("redux.sync.max.NaN.f32 %0, %0, 0xffffffff;" : "+f"(m));
+    const bool none = m == -INFINITY;
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < N; ++v) {
-        x[v] = expf(x[v] - m);       // (+inf - +inf and NaN rows: NaN)
+        x[v] = none ? 0.0f : bal_exp2((x[v] - m) * 1.44269502162933349609375f);
         sum += x[v];
     }
-    sum = warp_sum(sum);
-    nan = __any_sync(0xffffffffu, nan);
-    const float inv = (m == -INFINITY && !nan) ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int v = 0; v < N; ++v) x[v] = (m == -INFINITY && !nan) ? 0.0f : x[v] * inv;
+    return sum;
 }
+__device__ __forceinline__ float row_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 
 struct BalanceArgs {
     const float* logits;
@@ -127,26 +140,36 @@ struct BalanceArgs {
     const uint8_t* mask;
     SeqTable seq;
     int T, E, k, rows;      // rows per chunk
+    float coef;
     int32_t* head;          // error word, arrival counter
     int2* meta;             // per slot: valid tokens, error bits
     float* prob;            // [slots, E]
     int* hits;              // [slots, E]
+    float* part;            // [S][column blocks]
+    int32_t* counts;
+    float* mean_prob;       // or NULL
+    int32_t* tokens;        // [S + 1]
+    float* loss;
 };
 
-template <int N, bool VEC>
+// ONE: a single CTA has all rows and gives the results itself.
+template <int N, bool VEC, bool ONE>
 __global__ void __launch_bounds__(kBalThreads) k_balance_rows(BalanceArgs a) {
     pdl_begin();
     extern __shared__ float bal_smem[];
-    float* sp = bal_smem;                                   // [warps][E]
+    float* sp = bal_smem;                                           // [warps][E]
     int* sc = reinterpret_cast<int*>(bal_smem + kBalWarps * a.E);   // [E]
     __shared__ int s_n, s_bad;
+    __shared__ double s_sum[kBalWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = a.head[1] = 0;
+    if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = a.head[1] = 0;
     const int r0 = blockIdx.x * a.rows, r1 = min(a.T, r0 + a.rows);
-    for (int s = a.seq.find(r0); s < a.seq.S; ++s) {
+    double total = 0.0;       // ONE: this thread's part of the loss's sum
+    int used = 0, errors = 0;
+    for (int s = ONE ? 0 : a.seq.find(r0); s < a.seq.S; ++s) {
+        if (!ONE && a.seq.at(s) >= r1) break;
         const int b = max(a.seq.at(s), r0), e = min(a.seq.at(s + 1), r1);
-        if (a.seq.at(s) >= r1) break;
-        if (e <= b) continue;
+        if (!ONE && e <= b) continue;
         for (int c = threadIdx.x; c < a.E; c += kBalThreads) sc[c] = 0;
         if (threadIdx.x == 0) s_n = s_bad = 0;
         __syncthreads();
@@ -158,14 +181,16 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_rows(BalanceArgs a) {
             float x[N];
 #pragma unroll
             for (int v = 0; v < N; ++v) x[v] = nx[v];
+            int id = -1;
+            const bool on = !(a.mask && !__ldg(a.mask + r));
+            if (on && lane < a.k) id = __ldg(a.idx + (size_t)r * a.k + lane);
             if (r + kBalWarps < e) load_row<N, VEC>(a.logits + (size_t)(r + kBalWarps) * a.E, a.E, lane, nx);
-            if (a.mask && !__ldg(a.mask + r)) continue;
+            if (!on) continue;
             ++n;
-            row_softmax<N>(x);
+            const float inv = row_inverse(warp_sum(row_exp<N>(x)));
 #pragma unroll
-            for (int v = 0; v < N; ++v) acc[v] += x[v];
+            for (int v = 0; v < N; ++v) acc[v] = fmaf(x[v], inv, acc[v]);
             if (lane < a.k) {
-                const int id = __ldg(a.idx + (size_t)r * a.k + lane);
                 if ((unsigned)id < (unsigned)a.E)
                     atomicAdd(sc + id, 1);
                 else
@@ -180,55 +205,65 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_rows(BalanceArgs a) {
         if (lane == 0) atomicAdd(&s_n, n);
         __syncthreads();
         const size_t slot = (size_t)blockIdx.x + s;
+        const float inv_n = ONE && s_n > 0 ? 1.0f / (float)s_n : 0.0f;
         for (int c = threadIdx.x; c < a.E; c += kBalThreads) {
             float t = sp[c];
 #pragma unroll
             for (int w = 1; w < kBalWarps; ++w) t += sp[w * a.E + c];
-            a.prob[slot * a.E + c] = t;
-            a.hits[slot * a.E + c] = sc[c];
+            if (ONE) {
+                const float mp = t * inv_n;
+                a.counts[(size_t)s * a.E + c] = sc[c];
+                if (a.mean_prob) a.mean_prob[(size_t)s * a.E + c] = mp;
+                total += (double)((float)sc[c] * ((float)a.E / (float)a.k * inv_n) * mp);
+            } else {
+                a.prob[slot * a.E + c] = t;
+                a.hits[slot * a.E + c] = sc[c];
+            }
         }
-        if (threadIdx.x == 0) a.meta[slot] = make_int2(s_n, s_bad);
+        if (threadIdx.x == 0) {
+            if (ONE) {
+                a.tokens[s] = s_n;
+                used += s_n > 0;
+                errors |= s_bad | (a.seq.bad(s) ? FLAG_BOUNDS : 0);
+            } else {
+                a.meta[slot] = make_int2(s_n, s_bad);
+            }
+        }
         __syncthreads();
+    }
+    if (ONE) {
+        total = warp_sum(total);
+        if (lane == 0) s_sum[warp] = total;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kBalWarps; ++w) total += s_sum[w];
+            a.head[0] = errors;
+            a.tokens[a.seq.S] = used;
+            *a.loss = used > 0 ? (float)((double)a.coef * total / (double)used) : 0.0f;
+        }
     }
 }
 
 // CTA (column block of 32, sequence): 8 warps take every eighth chunk of the
 // sequence, lane = column; the eight sums are added in warp order.
-struct BalanceReduceArgs {
-    SeqTable seq;
-    int T, E, k, rows;
-    float coef;
-    int32_t* head;
-    const int2* meta;
-    const float* prob;
-    const int* hits;
-    float* part;            // [S][column blocks]
-    int32_t* counts;
-    float* mean_prob;       // or NULL
-    int32_t* tokens;        // [S + 1]
-    float* loss;
-};
-
-__global__ void __launch_bounds__(kBalThreads) k_balance_reduce(BalanceReduceArgs a) {
+__global__ void __launch_bounds__(kRedThreads) k_balance_reduce(BalanceArgs a) {
     pdl_begin();
-    __shared__ float sp[kBalWarps][33];
-    __shared__ int sc[kBalWarps][33];
-    __shared__ int sn[kBalWarps];
+    __shared__ float sp[kRedWarps][33];
+    __shared__ int sc[kRedWarps][33];
+    __shared__ int sn[kRedWarps];
     __shared__ bool s_last;
-    __shared__ double sred[kBalWarps];
-    __shared__ int sused[kBalWarps];
+    __shared__ double sred[kRedWarps];
+    __shared__ int sused[kRedWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int CB = (a.E + 31) / 32, cb = blockIdx.x, s = blockIdx.y;
     const int col = cb * 32 + lane;
     const int b = a.seq.at(s), e = a.seq.at(s + 1);
-    if (a.seq.off && threadIdx.x == 0 && cb == 0) {
-        const int rb = __ldg(a.seq.off + s), re = __ldg(a.seq.off + s + 1);
-        if (rb < 0 || re > a.T || re < rb) raise_flag(a.head, FLAG_BOUNDS);
-    }
+    if (threadIdx.x == 0 && cb == 0 && a.seq.bad(s)) raise_flag(a.head, FLAG_BOUNDS);
     const int c0 = b / a.rows, c1 = e > b ? (e - 1) / a.rows + 1 : c0;
     float p = 0.0f;
     int h = 0, n = 0, bad = 0;
-    for (int c = c0 + warp; c < c1; c += kBalWarps) {
+#pragma unroll 4
+    for (int c = c0 + warp; c < c1; c += kRedWarps) {
         const size_t slot = (size_t)c + s;
         const int2 m = a.meta[slot];
         n += m.x;
@@ -248,7 +283,7 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_reduce(BalanceReduceArg
         p = 0.0f;
         h = 0;
 #pragma unroll
-        for (int w = 0; w < kBalWarps; ++w) {
+        for (int w = 0; w < kRedWarps; ++w) {
             n += sn[w];
             p += sp[w][lane];
             h += sc[w][lane];
@@ -276,8 +311,8 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_reduce(BalanceReduceArg
     double sum = 0.0;
     int used = 0;
     const int total = a.seq.S * CB;
-    for (int i = threadIdx.x; i < total; i += kBalThreads) sum += (double)__ldcg(a.part + i);
-    for (int i = threadIdx.x; i < a.seq.S; i += kBalThreads) used += __ldcg(a.tokens + i) > 0;
+    for (int i = threadIdx.x; i < total; i += kRedThreads) sum += (double)__ldcg(a.part + i);
+    for (int i = threadIdx.x; i < a.seq.S; i += kRedThreads) used += __ldcg(a.tokens + i) > 0;
     sum = warp_sum(sum);
     used = warp_sum(used);
     if (lane == 0) {
@@ -288,7 +323,7 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_reduce(BalanceReduceArg
     if (threadIdx.x == 0) {
         sum = 0.0;
         used = 0;
-        for (int w = 0; w < kBalWarps; ++w) {
+        for (int w = 0; w < kRedWarps; ++w) {
             sum += sred[w];
             used += sused[w];
         }
@@ -331,12 +366,17 @@ struct RouteBackwardArgs {
 };
 
 // A warp takes `rows` consecutive rows, so that f of their sequence stays in
-// registers until the sequence changes.
+// registers until the sequence changes.  The balance term needs the softmax
+// only through sum e and sum e f (e = exp(x - max)), reduced together.  The
+// gates' terms are added to the stored row in memory: comparing each of the k
+// ids with a lane's columns in registers took two thirds of the instructions.
+constexpr int kRouteThreads = 256, kRouteWarps = kRouteThreads / 32;
+
 template <int N, bool VEC>
-__global__ void __launch_bounds__(kBalThreads) k_route_backward(RouteBackwardArgs a) {
+__global__ void __launch_bounds__(kRouteThreads) k_route_backward(RouteBackwardArgs a) {
     pdl_begin();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long first = ((long long)blockIdx.x * kBalWarps + warp) * a.rows;
+    const long long first = ((long long)blockIdx.x * kRouteWarps + warp) * a.rows;
     if (first >= a.T) return;
     const int r0 = (int)first, r1 = (int)min((long long)a.T, first + a.rows);
     int s = -1, s_end = r0;       // the sequence whose f is in registers ends at s_end
@@ -347,23 +387,15 @@ __global__ void __launch_bounds__(kBalThreads) k_route_backward(RouteBackwardArg
         float x[N];
 #pragma unroll
         for (int v = 0; v < N; ++v) x[v] = nx[v];
-        if (r + 1 < r1) load_row<N, VEC>(a.logits + (size_t)(r + 1) * a.E, a.E, lane, nx);
-        float add = 0.0f;
-        int id = -1;
-        if (a.dgates) {
-            float g = 0.0f, dg = 0.0f;
-            if (lane < a.k) {
-                id = __ldg(a.idx + (size_t)r * a.k + lane);
-                g = __ldg(a.gates + (size_t)r * a.k + lane);
-                dg = __ldg(a.dgates + (size_t)r * a.k + lane);
-                if ((unsigned)id >= (unsigned)a.E) {
-                    raise_flag(a.flag, FLAG_BAD_EXPERT);
-                    id = -1;
-                }
-            }
-            add = g * (dg - warp_sum(g * dg));
+        float g = 0.0f, dg = 0.0f;
+        int id = -1 - lane;       // (no expert, and no two lanes' alike)
+        if (a.dgates && lane < a.k) {
+            id = __ldg(a.idx + (size_t)r * a.k + lane);
+            g = __ldg(a.gates + (size_t)r * a.k + lane);
+            dg = __ldg(a.dgates + (size_t)r * a.k + lane);
         }
-        bool on = a.dloss && !(a.mask && !__ldg(a.mask + r));
+        if (r + 1 < r1) load_row<N, VEC>(a.logits + (size_t)(r + 1) * a.E, a.E, lane, nx);
+        const bool on = a.dloss && !(a.mask && !__ldg(a.mask + r));
         if (on && r >= s_end) {
             s = a.seq.find(r);
             s_end = s < a.seq.S ? a.seq.at(s + 1) : a.T;
@@ -383,31 +415,25 @@ __global__ void __launch_bounds__(kBalThreads) k_route_backward(RouteBackwardArg
                     f[v] = c < a.E ? (float)__ldg(cr + c) * fs : 0.0f;
                 }
             } else {
-#pragma unroll
-                for (int v = 0; v < N; ++v) f[v] = 0.0f;
                 if (!in) s_end = min(s_end, r + 1);
             }
         }
         if (on && w != 0.0f) {
-            row_softmax<N>(x);
-            float dot = 0.0f;
+            float sum = row_exp<N>(x), dot = 0.0f;
 #pragma unroll
             for (int v = 0; v < N; ++v) dot = fmaf(x[v], f[v], dot);
-            dot = warp_sum(dot);
 #pragma unroll
-            for (int v = 0; v < N; ++v) x[v] = w * x[v] * (f[v] - dot);
+            for (int o = 16; o > 0; o >>= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            }
+            const float inv = row_inverse(sum), wi = w * inv;
+            dot *= inv;
+#pragma unroll
+            for (int v = 0; v < N; ++v) x[v] = wi * x[v] * (f[v] - dot);
         } else {
 #pragma unroll
             for (int v = 0; v < N; ++v) x[v] = 0.0f;
-        }
-        if (a.dgates) {
-            for (int j = 0; j < a.k; ++j) {
-                const int ij = __shfl_sync(0xffffffffu, id, j);
-                const float aj = __shfl_sync(0xffffffffu, add, j);
-#pragma unroll
-                for (int v = 0; v < N; ++v)
-                    if (bal_col<VEC>(v, lane) == ij) x[v] += aj;
-            }
         }
         float* out = a.dlogits + (size_t)r * a.E;
         if (VEC) {
@@ -422,6 +448,29 @@ __global__ void __launch_bounds__(kBalThreads) k_route_backward(RouteBackwardArg
                 const int c = bal_col<false>(v, lane);
                 if (c < a.E) out[c] = x[v];
             }
+        }
+        if (a.dgates) {
+            float add = g * dg;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);   // (k <= 16)
+            add = g * (dg - add);
+            bool mine = lane < a.k;
+            if (mine && (unsigned)id >= (unsigned)a.E) {
+                raise_flag(a.flag, FLAG_BAD_EXPERT);
+                mine = false;
+            }
+            // an expert chosen twice: its first lane adds the terms in slot order
+            const uint32_t same = __match_any_sync(0xffffffffu, id);
+            if (__any_sync(0xffffffffu, same & (same - 1))) {
+                const float own = add;
+                for (int j = 0; j < a.k; ++j) {
+                    const float aj = __shfl_sync(0xffffffffu, own, j);
+                    if (j > lane && (same >> j & 1u)) add += aj;
+                }
+                mine = mine && lane == __ffs((int)same) - 1;
+            }
+            __syncwarp();        // the row is stored
+            if (mine) atomicAdd(out + id, add);      // (one per address: no order to depend on)
         }
     }
 }
@@ -445,6 +494,22 @@ static bool bal_vec(int E, const void* p, const void* q) {
     return E % 4 == 0 && ((uintptr_t)p | (uintptr_t)q) % 16 == 0;
 }
 
+template <int N, bool VEC, bool ONE>
+static cudaError_t launch_bal_rows(dim3 grid, size_t smem, cudaStream_t st, const BalanceArgs& a) {
+    auto kernel = k_balance_rows<N, VEC, ONE>;
+    if (smem > 48 * 1024) {
+        static PerContext cache;
+        const int ok = cache.get([&] {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (kBalWarps + 1) * kMaxExperts * 4) == cudaSuccess
+                       ? 1
+                       : -1;
+        });
+        if (ok < 0) return cudaErrorInvalidValue;
+    }
+    return launch_pdl(kernel, grid, dim3(kBalThreads), smem, st, a);
+}
+
 cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* seq_off, const uint8_t* mask,
                                 int T, int E, int k, int S, float coef, int32_t* counts, float* mean_prob,
                                 int32_t* tokens, float* loss, void* ws, cudaStream_t st) {
@@ -458,20 +523,19 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const i
         return e;
     }
     const BalanceWs L = balance_ws(T, E, S);
-    const SeqTable seq{seq_off, T, S};
-    const int rows = bal_chunk_rows(T);
-    BalanceArgs a{logits, idx, mask, seq, T, E, k, rows, head, (int2*)(w + L.meta), (float*)(w + L.prob),
-                  (int*)(w + L.hits)};
+    const bool one = T <= kBalSingleT && S <= kBalSingleS;
+    const int rows = one ? T : bal_chunk_rows(T);
+    BalanceArgs a{logits, idx, mask, SeqTable{seq_off, T, S}, T, E, k, rows, coef, head, (int2*)(w + L.meta),
+                  (float*)(w + L.prob), (int*)(w + L.hits), (float*)(w + L.part), counts, mean_prob, tokens, loss};
     const dim3 grid((unsigned)((T + rows - 1) / rows));
-    const size_t smem = (size_t)(kBalWarps + 1) * E * 4;      // at most 36 KB
-#define MOE_BAL_CALL(N, V) e = launch_pdl(k_balance_rows<N, V>, grid, dim3(kBalThreads), smem, st, a)
+    const size_t smem = (size_t)(kBalWarps + 1) * E * 4;      // at most 68 KB
+#define MOE_BAL_CALL(N, V)                                                                                    \
+    e = one ? launch_bal_rows<N, V, true>(grid, smem, st, a) : launch_bal_rows<N, V, false>(grid, smem, st, a)
     MOE_BAL_DISPATCH(E, bal_vec(E, logits, logits), MOE_BAL_CALL);
 #undef MOE_BAL_CALL
     count_launches(1);
-    if (e != cudaSuccess) return e;
-    BalanceReduceArgs b{seq, T, E, k, rows, coef, head, (const int2*)(w + L.meta), (const float*)(w + L.prob),
-                        (const int*)(w + L.hits), (float*)(w + L.part), counts, mean_prob, tokens, loss};
-    e = launch_pdl(k_balance_reduce, dim3((unsigned)((E + 31) / 32), (unsigned)S), dim3(kBalThreads), 0, st, b);
+    if (e != cudaSuccess || one) return e;
+    e = launch_pdl(k_balance_reduce, dim3((unsigned)((E + 31) / 32), (unsigned)S), dim3(kRedThreads), 0, st, a);
     count_launches(1);
     return e;
 }
@@ -482,12 +546,12 @@ cudaError_t launch_route_backward(const float* logits, const int32_t* idx, const
                                   float* dlogits, int32_t* flag, cudaStream_t st) {
     if (T == 0) return cudaSuccess;
     // one row per warp until the SMs are full, then up to 8
-    const int rows = std::min(8, std::max(1, T / (148 * 32)));
+    const int rows = std::min(8, std::max(1, T / (148 * 48)));
     RouteBackwardArgs a{logits, idx, gates, dgates, dloss, counts, tokens, mask, SeqTable{seq_off, T, S}, T, E, k,
                         rows, coef, dlogits, flag};
-    const dim3 grid((unsigned)((T + rows * kBalWarps - 1) / (rows * kBalWarps)));
+    const dim3 grid((unsigned)((T + rows * kRouteWarps - 1) / (rows * kRouteWarps)));
     cudaError_t e;
-#define MOE_BAL_CALL(N, V) e = launch_pdl(k_route_backward<N, V>, grid, dim3(kBalThreads), 0, st, a)
+#define MOE_BAL_CALL(N, V) e = launch_pdl(k_route_backward<N, V>, grid, dim3(kRouteThreads), 0, st, a)
     MOE_BAL_DISPATCH(E, bal_vec(E, logits, dlogits), MOE_BAL_CALL);
 #undef MOE_BAL_CALL
     count_launches(1);

@@ -13,53 +13,91 @@ constexpr int kCkThreads = 256;
 // items, a grid stride apart, and issues their loads together.
 constexpr int kCkUnroll = 4;
 
+// Row of an item (8 of a row's K8).  Contiguous rows (FLAT) need none: the
+// strided form divides, in 32 bits where the count allows.
+__device__ __forceinline__ long long ck_row(long long i, int K8, bool small) {
+    return small ? (long long)((uint32_t)i / (uint32_t)K8) : i / K8;
+}
+
+// The arithmetic is on pairs of bf16 as far as it goes: |x| and the maximum on
+// the bits, x 2^-e exactly (below bf16's normal range the code is 0 either way),
+// and only the last step, to E4M3, from fp32.  With fp32 throughout the kernel
+// was bound by its instructions (59 us for 16384 x 4096).
+template <bool FLAT>
 __global__ void __launch_bounds__(kCkThreads)
     k_ckpt_pack(const __nv_bfloat16* __restrict__ x, long long ldx, long long items, int K8,
                 uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
     pdl_begin();
     const long long stride = (long long)gridDim.x * kCkThreads;
+    const bool small = items >> 31 == 0;
     // (items and stride are multiples of 16: the lanes of a block agree)
-    for (long long i0 = blockIdx.x * (long long)kCkThreads + threadIdx.x; i0 - (threadIdx.x & 31) < items; i0 += stride * kCkUnroll) {
+    for (long long i0 = blockIdx.x * (long long)kCkThreads + threadIdx.x; i0 - (threadIdx.x & 31) < items;
+         i0 += stride * kCkUnroll) {
         uint4 q[kCkUnroll];
 #pragma unroll
         for (int u = 0; u < kCkUnroll; ++u) {
             const long long i = i0 + u * stride;
             q[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < items) {
-                const long long t = i / K8;
-                q[u] = __ldg(reinterpret_cast<const uint4*>(x + t * ldx + (i - t * K8) * 8));
+            if (i >= items) continue;
+            long long src = i * 8;
+            if (!FLAT) {
+                const long long t = ck_row(i, K8, small);
+                src = t * ldx + (i - t * K8) * 8;
             }
+            q[u] = __ldg(reinterpret_cast<const uint4*>(x + src));
         }
 #pragma unroll
         for (int u = 0; u < kCkUnroll; ++u) {
             const long long i = i0 + u * stride;
-            float v[8];
-            bf16x8_values(q[u], v);
-            float amax = 0.0f;
-            uint32_t bad = 0;        // bit j: value j is a NaN or an infinity
+            const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+            // the block's maximum magnitude; NaN where it holds one
+            auto max2 = [](uint32_t a, uint32_t b) {
+                uint32_t r;
+                asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+                return r;
+            };
+            uint32_t m = max2(max2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float a = fabsf(v[j]);
-                if (a <= 3.4028235e38f)
-                    amax = fmaxf(amax, a);
-                else
-                    bad |= 1u << j;
+            for (int o = 1; o < 16; o <<= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, o));
+            m = max2(m, m >> 16) & 0x7fffu;
+            float amax = __uint_as_float(m << 16);
+            const bool odd = m > 0x7f60u;       // above 448 * 2^119 (e = 120), or not finite
+            if (__any_sync(0xffffffffu, odd)) {
+                // the maximum of the finite values
+                amax = 0.0f;
+                float v[8];
+                bf16x8_values(q[u], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]) <= 3.4028235e38f ? fabsf(v[j]) : 0.0f);
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             }
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             if (i >= items) continue;
             const int e = ckpt_exponent(amax);
-            const float inv = ckpt_pow2(-e);
-            const float top = e >= 120 ? 240.0f : 448.0f;
+            uint2 c;
+            if (!odd) {
+                const uint32_t inv = (__float_as_uint(ckpt_pow2(-e)) >> 16) * 0x00010001u;     // exact in bf16
+                float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = fminf(fmaxf(v[j] * inv, -top), top);
-            uint2 c = make_uint2(e4m3x4_code(v[0], v[1], v[2], v[3]), e4m3x4_code(v[4], v[5], v[6], v[7]));
-            if (bad) {
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t p;
+                    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(w[j]), "r"(inv));
+                    v[2 * j] = __uint_as_float(p << 16);
+                    v[2 * j + 1] = __uint_as_float(p & 0xffff0000u);
+                }
+                c = make_uint2(e4m3x4_code(v[0], v[1], v[2], v[3]), e4m3x4_code(v[4], v[5], v[6], v[7]));
+            } else {
+                const float inv = ckpt_pow2(-e), top = e >= 120 ? 240.0f : 448.0f;
+                float v[8], r[8];
+                bf16x8_values(q[u], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[j] = fminf(fmaxf(v[j] * inv, -top), top);
+                c = make_uint2(e4m3x4_code(r[0], r[1], r[2], r[3]), e4m3x4_code(r[4], r[5], r[6], r[7]));
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (bad >> j & 1u) {
-                        uint32_t& w = j < 4 ? c.x : c.y;
-                        w = (w & ~(0xffu << (8 * (j & 3)))) | (0x7fu << (8 * (j & 3)));
+                    if (!(fabsf(v[j]) <= 3.4028235e38f)) {
+                        uint32_t& cw = j < 4 ? c.x : c.y;
+                        cw = (cw & ~(0xffu << (8 * (j & 3)))) | (0x7fu << (8 * (j & 3)));
                     }
             }
             *reinterpret_cast<uint2*>(codes + i * 8) = c;
@@ -68,11 +106,13 @@ __global__ void __launch_bounds__(kCkThreads)
     }
 }
 
+template <bool FLAT>
 __global__ void __launch_bounds__(kCkThreads)
     k_ckpt_unpack(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long items, int K8,
                   __nv_bfloat16* __restrict__ x, long long ldx) {
     pdl_begin();
     const long long stride = (long long)gridDim.x * kCkThreads;
+    const bool small = items >> 31 == 0;
     for (long long i0 = blockIdx.x * (long long)kCkThreads + threadIdx.x; i0 < items; i0 += stride * kCkUnroll) {
         uint2 c[kCkUnroll];
         uint32_t s[kCkUnroll];
@@ -90,8 +130,12 @@ __global__ void __launch_bounds__(kCkThreads)
             if (i >= items) break;
             float v[8];
             ckpt_values8(c[u], ckpt_scale(s[u]), v);
-            const long long t = i / K8;
-            *reinterpret_cast<uint4*>(x + t * ldx + (i - t * K8) * 8) = bf16x8_rn(v);
+            long long dst = i * 8;
+            if (!FLAT) {
+                const long long t = ck_row(i, K8, small);
+                dst = t * ldx + (i - t * K8) * 8;
+            }
+            *reinterpret_cast<uint4*>(x + dst) = bf16x8_rn(v);
         }
     }
 }
@@ -110,6 +154,7 @@ __global__ void __launch_bounds__(kCkThreads)
     pdl_begin();
     constexpr int U = 2;
     const int I8 = I / 8, KB = I / 128;
+    const bool small = items >> 31 == 0;
     const long long stride = (long long)gridDim.x * kCkThreads;
     for (long long i0 = blockIdx.x * (long long)kCkThreads + threadIdx.x; i0 < items; i0 += stride * U) {
         uint2 cg[U], cu[U];
@@ -121,7 +166,7 @@ __global__ void __launch_bounds__(kCkThreads)
         for (int u = 0; u < U; ++u) {
             const long long i = i0 + u * stride;
             if (i < items) {
-                t[u] = i / I8;
+                t[u] = ck_row(i, I8, small);
                 c8[u] = (int)(i - t[u] * I8);
                 const uint8_t* row = codes + t[u] * 2 * I + c8[u] * 8;
                 const uint8_t* srow = scales + t[u] * 2 * KB + (c8[u] >> 4);
@@ -168,7 +213,7 @@ cudaError_t launch_ckpt_pack(const void* x, long long ldx, int T, int K, uint8_t
                              cudaStream_t st) {
     if (T == 0) return cudaSuccess;
     const long long items = (long long)T * (K / 8);
-    const cudaError_t e = launch_pdl(k_ckpt_pack, ck_grid(items, kCkUnroll), dim3(kCkThreads), 0, st,
+    const cudaError_t e = launch_pdl(ldx == K ? k_ckpt_pack<true> : k_ckpt_pack<false>, ck_grid(items, kCkUnroll), dim3(kCkThreads), 0, st,
                                      (const __nv_bfloat16*)x, ldx, items, K / 8, codes, scales);
     count_launches(1);
     return e;
@@ -178,7 +223,7 @@ cudaError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int 
                                cudaStream_t st) {
     if (T == 0) return cudaSuccess;
     const long long items = (long long)T * (K / 8);
-    const cudaError_t e = launch_pdl(k_ckpt_unpack, ck_grid(items, kCkUnroll), dim3(kCkThreads), 0, st, codes, scales,
+    const cudaError_t e = launch_pdl(ldx == K ? k_ckpt_unpack<true> : k_ckpt_unpack<false>, ck_grid(items, kCkUnroll), dim3(kCkThreads), 0, st, codes, scales,
                                      items, K / 8, (__nv_bfloat16*)x, ldx);
     count_launches(1);
     return e;

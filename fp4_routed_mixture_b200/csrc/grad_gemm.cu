@@ -887,6 +887,7 @@ __global__ void __launch_bounds__(1024) k_router_bias(const float* __restrict__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
     float v = 0.0f;
     if (e < E)
+#pragma unroll 8
         for (int i = warp; i < n; i += 32) v += __ldg(part + (size_t)i * E + e);
     s[warp][lane] = v;
     __syncthreads();
