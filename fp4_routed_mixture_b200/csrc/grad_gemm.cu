@@ -80,6 +80,7 @@ struct GradShared {
     uint8_t ops[GradCfg<MODE>::STAGES][GradCfg<MODE>::OPS];      // 1024-byte aligned
     uint8_t out[GG_EPI_WARPS][GG_OUT];               // epilogue: 32 rows of 128 bytes per warp
     uint64_t landed[GradCfg<MODE>::STAGES];          // leader: TMA bytes of both CTAs
+    uint64_t tail_landed[GradCfg<MODE>::STAGES];     // a stage with a tail: those of this CTA
     uint64_t tail[GradCfg<MODE>::STAGES];            // its rows behind the group are cleared
     uint64_t peer[GradCfg<MODE>::STAGES];            // leader: those of the other CTA are
     uint64_t empty[GradCfg<MODE>::STAGES];
@@ -211,6 +212,12 @@ __device__ __forceinline__ void gg_rows(const GradArgs& a, int g, int& r0, int& 
         r1 = min(max(__ldg(a.offsets + g + 1), r0), a.R);
     }
 }
+// Tile i of a group, row by row.  (Bands of 4 or 8 columns, which would share
+// both operands' panels in L2 among the tiles in flight, measured the same.)
+__device__ __forceinline__ void gg_tile(const GradArgs& a, int i, int& m0, int& n0) {
+    m0 = (i / a.NT) * GG_TILE;
+    n0 = (i % a.NT) * GG_TILE;
+}
 // (a group without rows still has one stage, of zeros)
 __device__ __forceinline__ int gg_steps(int rows) { return max(1, (int)(((long long)rows + GG_K - 1) / GG_K)); }
 
@@ -261,8 +268,7 @@ struct Walk {
         }
         const int per = a.MT * a.NT, i = t % per;
         s.g = t / per;
-        s.m0 = (i / a.NT) * GG_TILE;
-        s.n0 = (i % a.NT) * GG_TILE;
+        gg_tile(a, i, s.m0, s.n0);
         gg_rows(a, s.g, s.r0, s.r1);
         const int steps = gg_steps(s.r1 - s.r0);
         s.s0 = 0;
@@ -319,6 +325,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sh.landed[s]), 1);
+            mbar_init(smem_u32(&sh.tail_landed[s]), 1);
             mbar_init(smem_u32(&sh.tail[s]), GG_TAIL_WARPS);
             mbar_init(smem_u32(&sh.peer[s]), GG_TAIL_WARPS);
             mbar_init(smem_u32(&sh.empty[s]), 1);
@@ -401,15 +408,16 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
 
     // Stages with rows behind their group's last one (the last stage of a group
     // with another row count than a multiple of 64): dy and x of other rows have
-    // landed there and are cleared (rows behind R read as 0).  Each CTA then
-    // counts its own bytes.  tails: parity of each stage's next clearing.
-    uint32_t tails = 0;
+    // landed there and are cleared (rows behind R read as 0).  Each CTA counts its
+    // own bytes for them, on other barriers.  lands, tails: parity of the next use
+    // of each stage's barriers of either kind.
+    uint32_t lands = 0, tails = 0;
     auto has_tail = [&](const Segment& s, int st) {
         return MODE == GM_WGRAD && s.r1 < a.R && s.r1 - s.r0 - st * GG_K < GG_K;
     };
-    auto tail_parity = [&]() {
-        const uint32_t p = tails >> stage & 1u;
-        tails ^= 1u << stage;
+    auto next_parity = [&](uint32_t& bits) {
+        const uint32_t p = bits >> stage & 1u;
+        bits ^= 1u << stage;
         return p;
     };
 
@@ -421,7 +429,6 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             // waits here run to their limit even when another role has given
             // up: "empty" reaches both CTAs, so both have then issued the same
             // stages, and the leader's last waits cover the copies of both.)
-            uint32_t filled = 0, parity = 0;      // bit s: this CTA's barrier of stage s is armed, and its phase
             constexpr uint32_t bytes = (AP + BP) * GG_PLANE;
             for (Steps s(walk0); s.on; s.advance()) {
                 if (!mbar_wait_for<false>(smem_u32(&sh.empty[stage]), phase ^ 1u, a.wait_ns, nullptr)) {
@@ -429,17 +436,16 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                     break;
                 }
                 const bool tail = has_tail(s.seg, s.st);
-                const uint32_t own = smem_u32(&sh.landed[stage]);
-                const uint32_t bar = rank == 0 || tail ? own : gg_peer(own, 0);
+                uint32_t bar = smem_u32(tail ? &sh.tail_landed[stage] : &sh.landed[stage]);
+                if (rank == 0 || tail) {
+                    mbar_expect_tx(bar, tail ? bytes : 2 * bytes);
+                    next_parity(tail ? tails : lands);
+                } else {
+                    bar = gg_peer(bar, 0);
+                }
                 uint32_t dst = smem_u32(sh.ops[stage]);
                 const int r = s.seg.r0 + s.st * GG_K;
                 const int m = s.seg.m0 + GG_HALF * (int)rank, n = s.seg.n0 + GG_HALF * (int)rank;
-                if (rank == 0 || tail) {
-                    const uint32_t p = rank == 0 ? phase : tail_parity();
-                    mbar_expect_tx(own, tail ? bytes : 2 * bytes);
-                    filled |= 1u << stage;
-                    parity = (parity & ~(1u << stage)) | (p << stage);
-                }
 #pragma unroll
                 for (int p = 0; p < AP; ++p, dst += GG_PLANE) {
                     if (MODE == GM_RDX) {
@@ -456,8 +462,12 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                 }
                 next_stage();
             }
-            for (int s = 0; s < STAGES; ++s)
-                if (filled >> s & 1u) final_wait(smem_u32(&sh.landed[s]), parity >> s & 1u);
+            // (a barrier's last use has the other parity than its next; one never used
+            // passes as the phase in front of the first)
+            for (int s = 0; s < STAGES; ++s) {
+                final_wait(smem_u32(&sh.landed[s]), (lands >> s & 1u) ^ 1u);
+                final_wait(smem_u32(&sh.tail_landed[s]), (tails >> s & 1u) ^ 1u);
+            }
         } else if (warp == 1 && lane == 0) {
             // ---------------- MMA issuer ----------------
             if (rank == 0) {
@@ -478,10 +488,12 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                         tc_fence_after();
                         const uint32_t d = tmem + buf * GG_TILE;
                         for (int s = st; s < st1; ++s) {
-                            bool in = wait(smem_u32(&sh.landed[stage]), phase);
-                            if (in && has_tail(seg, s)) {
-                                const uint32_t p = tail_parity();
+                            bool in;
+                            if (has_tail(seg, s)) {
+                                const uint32_t p = next_parity(tails);
                                 in = wait(smem_u32(&sh.tail[stage]), p) && wait(smem_u32(&sh.peer[stage]), p);
+                            } else {
+                                in = wait(smem_u32(&sh.landed[stage]), next_parity(lands));
                             }
                             if (!in) {
                                 give_up();
@@ -537,17 +549,13 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         gg_regs_down<GG_REGS_LOAD>();
         if (MODE == GM_WGRAD && a.offsets) {
             // ---------------- rows behind a group's last one ----------------
-            // The leader's barriers pass every stage, the other CTA's only these.
             const int t = threadIdx.x - 32 * GG_TAIL_WARP0;
             for (Steps s(walk0); s.on; s.advance()) {
-                const bool tail = has_tail(s.seg, s.st);
-                if (rank == 0 || tail) {
-                    if (!warp_wait(smem_u32(&sh.landed[stage]), rank == 0 ? phase : tail_parity())) {
+                if (has_tail(s.seg, s.st)) {
+                    if (!warp_wait(smem_u32(&sh.tail_landed[stage]), next_parity(tails))) {
                         give_up();
                         break;
                     }
-                }
-                if (tail) {
                     const int valid = s.seg.r1 - s.seg.r0 - s.st * GG_K;
                     const uint32_t dst = smem_u32(sh.ops[stage]);
                     for (int i = t; i < Cfg::OPS / 16; i += 32 * GG_TAIL_WARPS)
@@ -693,8 +701,9 @@ __global__ void __launch_bounds__(256) k_grad_fixup(GradArgs a, int pairs) {
     __syncthreads();
     const int n = s_n;
     if (n == 1) return;        // one pair computed the whole tile
-    const int t = a.full + i, ti = t % per;
-    const int m0 = (ti / a.NT) * GG_TILE, n0 = (ti % a.NT) * GG_TILE;
+    const int t = a.full + i;
+    int m0, n0;
+    gg_tile(a, t % per, m0, n0);
     float* out = a.c + ((size_t)(t / per) * a.M + m0) * a.N + n0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -846,23 +855,44 @@ __global__ void __launch_bounds__(kSplitThreads) k_grad_prepare(PrepareArgs a) {
     b -= a.w_ctas;
     // The checkpoint's values, 8 codes per item.
     constexpr int U = 4;
-    const int K8 = a.K / 8;
-    const long long stride = (long long)(gridDim.x - a.dl_ctas - a.w_ctas) * kSplitThreads;
+    const long long ctas = gridDim.x - a.dl_ctas - a.w_ctas;
+    if (a.perm) {
+        // a warp per row: its table entry is resolved once
+        const int lane = threadIdx.x & 31, K8 = a.K / 8;
+        for (long long r = (long long)b * (kSplitThreads / 32) + (threadIdx.x >> 5); r < a.R;
+             r += ctas * (kSplitThreads / 32)) {
+            const int v = __ldg(a.perm + r), x = v < 0 ? 0 : v / a.k_div;
+            const long long src = (long long)(x < a.xrows ? x : 0) * K8;      // (bad entries: row 0)
+            for (int c0 = lane; c0 < K8; c0 += 32 * U) {
+                uint2 c[U];
+                uint32_t s[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * u < K8) {
+                        c[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + (src + c0 + 32 * u) * 8));
+                        s[u] = __ldg(a.scales + ((src + c0 + 32 * u) >> 4));
+                    }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * u < K8) {
+                        float o[8];
+                        ckpt_values8(c[u], ckpt_scale(s[u]), o);
+                        reinterpret_cast<uint4*>(a.xb)[r * K8 + c0 + 32 * u] = bf16x8_rn(o);
+                    }
+            }
+        }
+        return;
+    }
+    const long long stride = ctas * kSplitThreads;
     for (long long i0 = (long long)b * kSplitThreads + threadIdx.x; i0 < a.items; i0 += stride * U) {
         uint2 c[U];
         uint32_t s[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long i = i0 + u * stride;
-            long long src = i;
             if (i >= a.items) continue;
-            if (a.perm) {
-                const int r = a.items >> 31 ? (int)(i / K8) : (int)((uint32_t)i / (uint32_t)K8);
-                const int v = __ldg(a.perm + r), x = v < 0 ? 0 : v / a.k_div;
-                src = (long long)(x < a.xrows ? x : 0) * K8 + (i - (long long)r * K8);    // (bad entries: row 0)
-            }
-            c[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + src * 8));
-            s[u] = __ldg(a.scales + (src >> 4));
+            c[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + i * 8));
+            s[u] = __ldg(a.scales + (i >> 4));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
