@@ -412,10 +412,13 @@ def _arg(t, name: str, dtype, shape, dev, strided: bool = False):
     whose rows may lie further apart than their length."""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _bad(f"{name} must be a CUDA tensor")
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return t.data_ptr()
     if t.dtype is not dtype:
         _bad(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:

@@ -26,7 +26,8 @@
 //                 contraction runs over smem rows, except A of GM_RDX)
 //   warp 1        (leader CTA) issues the MMAs
 //   warp 2        GM_WGRAD through perm: checks the table
-//   warps 4-7     GM_WGRAD: clear the rows behind a group's last one
+//   warps 4-7     GM_WGRAD: clear the rows behind a group's last one; else the
+//                 sums of dbias
 //   warps 8-15    epilogue, from two 256-column accumulators in TMEM
 // Work: pair p takes the tiles p, p + P, ... of the first floor(tiles / P) P
 // ones whole; the remaining tiles are cut so that the last round is not left to
@@ -88,7 +89,37 @@ struct GradShared {
     uint32_t tmem_base;
     int32_t abort;
     int32_t rem_pre[GG_MAX_PAIRS + 1];               // chunks in front of each split tile
+    float bias[4][32];
 };
+
+// dbias: column sums over the row blocks that k_grad_prepare summed.  128 threads
+// take 32 columns: warp w every fourth block, then the warps in order.  (The
+// warps of the router's GEMMs that have no other work do it, 4-7, or a kernel of
+// its own where no GEMM runs: the same order and bits.)
+struct BiasArgs {
+    const float* part;       // [n][E], or NULL
+    int n, E;
+    float* db;
+    int accumulate;
+};
+__device__ __forceinline__ void grad_bias(const BiasArgs& a, int block, int t, float (*s)[32]) {
+    const int w = t >> 5, lane = t & 31, e = block * 32 + lane;
+    float v = 0.0f;
+    if (e < a.E)
+#pragma unroll 8
+        for (int i = w; i < a.n; i += 4) v += __ldg(a.part + (size_t)i * a.E + e);
+    s[w][lane] = v;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (w == 0 && e < a.E) {
+        v = ((s[0][lane] + s[1][lane]) + s[2][lane]) + s[3][lane];
+        a.db[e] = a.accumulate ? a.db[e] + v : v;
+    }
+}
+__global__ void __launch_bounds__(128) k_router_bias(BiasArgs a) {
+    pdl_begin();
+    __shared__ float s[4][32];
+    grad_bias(a, blockIdx.x, threadIdx.x, s);
+}
 
 struct GradArgs {
     const int32_t* offsets;    // groups of rows, or NULL
@@ -101,6 +132,7 @@ struct GradArgs {
     float* c;                  // (GM_RDX stores through its map alone)
     int accumulate;
     float* part;               // [pairs][2][256][256]
+    BiasArgs bias;             // GM_RDW, GM_RDX
     int32_t* flag;
     uint64_t wait_ns;
 };
@@ -547,6 +579,12 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         __syncwarp();
     } else if (warp < GG_EPI_WARP0) {
         gg_regs_down<GG_REGS_LOAD>();
+        if (MODE != GM_WGRAD && a.bias.part) {
+            for (int b = blockIdx.x; b * 32 < a.bias.E; b += gridDim.x) {
+                grad_bias(a.bias, b, threadIdx.x - 32 * GG_TAIL_WARP0, sh.bias);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
+        }
         if (MODE == GM_WGRAD && a.offsets) {
             // ---------------- rows behind a group's last one ----------------
             const int t = threadIdx.x - 32 * GG_TAIL_WARP0;
@@ -909,25 +947,6 @@ static unsigned prepare_ctas(long long items) {
     return (unsigned)std::min<long long>((items + 4 * kSplitThreads - 1) / (4 * kSplitThreads), 148 * 32);
 }
 
-// dbias: the CTAs' column sums, warps take every 32nd, then in warp order.
-__global__ void __launch_bounds__(1024) k_router_bias(const float* __restrict__ part, int n, int E, float* db,
-                                                      int accumulate) {
-    pdl_begin();
-    __shared__ float s[32][33];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
-    float v = 0.0f;
-    if (e < E)
-#pragma unroll 8
-        for (int i = warp; i < n; i += 32) v += __ldg(part + (size_t)i * E + e);
-    s[warp][lane] = v;
-    __syncthreads();
-    if (warp == 0 && e < E) {
-        v = 0.0f;
-        for (int w = 0; w < 32; ++w) v += s[w][lane];
-        db[e] = accumulate ? db[e] + v : v;
-    }
-}
-
 // ---- host -----------------------------------------------------------------------------
 template <int MODE>
 static size_t grad_smem() { return sizeof(GradShared<MODE>) + 1024; }
@@ -1159,6 +1178,7 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
     a.N = H;
     a.flag = flag;
     a.wait_ns = wait_ns;
+    BiasArgs bias{s.bias_part, s.dl_ctas, E, db, accumulate};
     CUtensorMap a_map, b_map;
     if (e == cudaSuccess && dw) {
         e = bf16_map(s.dlp, Ep, T, Ep, 3, GG_K, &a_map);
@@ -1169,6 +1189,8 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
         d.M = E;
         d.accumulate = accumulate;
         d.part = (float*)(b + L.part);
+        d.bias = bias;
+        bias.part = nullptr;
         e = launch_grad<GM_RDW>(d, a_map, b_map, dw, st);
     }
     if (e == cudaSuccess && dx) {
@@ -1177,11 +1199,12 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
         if (e != cudaSuccess) return e;
         a.R = E;
         a.M = T;
+        a.bias = bias;
+        bias.part = nullptr;
         e = launch_grad<GM_RDX>(a, a_map, b_map, dx, st);
     }
-    if (e == cudaSuccess && db) {
-        e = launch_pdl(k_router_bias, dim3((unsigned)((E + 31) / 32)), dim3(1024), 0, st, (const float*)s.bias_part,
-                       s.dl_ctas, E, db, accumulate);
+    if (e == cudaSuccess && bias.part) {
+        e = launch_pdl(k_router_bias, dim3((unsigned)((E + 31) / 32)), dim3(128), 0, st, bias);
         count_launches(1);
     }
     return e;
