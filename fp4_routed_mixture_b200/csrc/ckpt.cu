@@ -152,55 +152,39 @@ __global__ void __launch_bounds__(kCkThreads)
                       const __nv_bfloat16* __restrict__ dh, long long lddh, long long items, int I,
                       __nv_bfloat16* __restrict__ dgu, __nv_bfloat16* __restrict__ h) {
     pdl_begin();
-    constexpr int U = 2;
     const int I8 = I / 8, KB = I / 128;
     const bool small = items >> 31 == 0;
     const long long stride = (long long)gridDim.x * kCkThreads;
-    for (long long i0 = blockIdx.x * (long long)kCkThreads + threadIdx.x; i0 < items; i0 += stride * U) {
-        uint2 cg[U], cu[U];
-        uint32_t sg[U], su[U];
-        uint4 d[U];
-        long long t[U];
-        int c8[U];
+    // (one item in flight per thread, at full occupancy: 56 us for 16384 x 2048
+    // with h; two and four at fewer threads 61 and 64)
+    for (long long i = blockIdx.x * (long long)kCkThreads + threadIdx.x; i < items; i += stride) {
+        const long long t = ck_row(i, I8, small);
+        const int c8 = (int)(i - t * I8);
+        const uint8_t* row = codes + t * 2 * I + c8 * 8;
+        const uint8_t* srow = scales + t * 2 * KB + (c8 >> 4);
+        const uint2 cg = __ldg(reinterpret_cast<const uint2*>(row)), cu = __ldg(reinterpret_cast<const uint2*>(row + I));
+        const uint32_t sg = __ldg(srow), su = __ldg(srow + KB);
+        const uint4 d = __ldg(reinterpret_cast<const uint4*>(dh + t * lddh + c8 * 8));
+        float g[8], up[8], dv[8], og[8], ou[8], oh[8];
+        ckpt_values8(cg, ckpt_scale(sg), g);
+        ckpt_values8(cu, ckpt_scale(su), up);
+        bf16x8_values(d, dv);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long i = i0 + u * stride;
-            if (i < items) {
-                t[u] = ck_row(i, I8, small);
-                c8[u] = (int)(i - t[u] * I8);
-                const uint8_t* row = codes + t[u] * 2 * I + c8[u] * 8;
-                const uint8_t* srow = scales + t[u] * 2 * KB + (c8[u] >> 4);
-                cg[u] = __ldg(reinterpret_cast<const uint2*>(row));
-                cu[u] = __ldg(reinterpret_cast<const uint2*>(row + I));
-                sg[u] = __ldg(srow);
-                su[u] = __ldg(srow + KB);
-                d[u] = __ldg(reinterpret_cast<const uint4*>(dh + t[u] * lddh + c8[u] * 8));
-            }
+        for (int j = 0; j < 8; ++j) {
+            const float e = __expf(-fabsf(g[j]));
+            const float r = __fdividef(1.0f, 1.0f + e);
+            const float er = e * r;
+            const float s = g[j] >= 0.0f ? r : er;       // NaN: er, a NaN
+            const float q = g[j] >= 0.0f ? er : r;       // 1 - s
+            const float a = g[j] * s;
+            og[j] = dv[j] * up[j] * fmaf(a, q, s);
+            ou[j] = dv[j] * a;
+            oh[j] = a * up[j];
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u * stride >= items) break;
-            float g[8], up[8], dv[8], og[8], ou[8], oh[8];
-            ckpt_values8(cg[u], ckpt_scale(sg[u]), g);
-            ckpt_values8(cu[u], ckpt_scale(su[u]), up);
-            bf16x8_values(d[u], dv);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float e = __expf(-fabsf(g[j]));
-                const float r = __fdividef(1.0f, 1.0f + e);
-                const float er = e * r;
-                const float s = g[j] >= 0.0f ? r : er;       // NaN: er, a NaN
-                const float q = g[j] >= 0.0f ? er : r;       // 1 - s
-                const float a = g[j] * s;
-                og[j] = dv[j] * up[j] * fmaf(a, q, s);
-                ou[j] = dv[j] * a;
-                oh[j] = a * up[j];
-            }
-            __nv_bfloat16* o = dgu + t[u] * 2 * I + c8[u] * 8;
-            *reinterpret_cast<uint4*>(o) = bf16x8_rn(og);
-            *reinterpret_cast<uint4*>(o + I) = bf16x8_rn(ou);
-            if (H) *reinterpret_cast<uint4*>(h + t[u] * I + c8[u] * 8) = bf16x8_rn(oh);
-        }
+        __nv_bfloat16* o = dgu + t * 2 * I + c8 * 8;
+        *reinterpret_cast<uint4*>(o) = bf16x8_rn(og);
+        *reinterpret_cast<uint4*>(o + I) = bf16x8_rn(ou);
+        if (H) *reinterpret_cast<uint4*>(h + t * I + c8 * 8) = bf16x8_rn(oh);
     }
 }
 
@@ -233,7 +217,7 @@ cudaError_t launch_ckpt_swiglu_backward(const uint8_t* codes, const uint8_t* sca
                                         int T, int I, void* dgu, void* h, cudaStream_t st) {
     if (T == 0) return cudaSuccess;
     const long long items = (long long)T * (I / 8);
-    const dim3 grid = ck_grid(items, 2);
+    const dim3 grid = ck_grid(items, 1);
     cudaError_t e;
     if (h)
         e = launch_pdl(k_ckpt_swiglu_bwd<true>, grid, dim3(kCkThreads), 0, st, codes, scales, (const __nv_bfloat16*)dh,

@@ -236,6 +236,11 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
                               const int32_t* offsets, const int32_t* perm, int k, int R, int rows, int N, int K, int G,
                               float* dw, int accumulate, void* ws, uint64_t wait_ns, cudaStream_t st);
 size_t router_backward_workspace_bytes(int T, int H, int E);
+// Calls of at most kRouterGradSmallT tokens run on the CUDA cores (router_grad_small.cu).
+constexpr int kRouterGradSmallT = 64;
+cudaError_t launch_router_grad_small(const float* dl, const void* x, const uint8_t* codes, const uint8_t* scales,
+                                     const float* w, int T, int H, int E, void* dx, float* dw, float* db,
+                                     int accumulate, int32_t* flag, cudaStream_t st);
 cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t* codes, const uint8_t* scales,
                                    const float* w, int T, int H, int E, void* dx, float* dw, float* db, int accumulate,
                                    void* ws, uint64_t wait_ns, cudaStream_t st);
