@@ -60,6 +60,7 @@ std::atomic<int> g_tc_min_rows{0};         // tensor-core row threshold; 0 = aut
 std::atomic<int> g_tc_pair{0};             // tensor-core GEMM in SM pairs (cta_group::2) where the shape allows
 std::atomic<int> g_wait_limit_us{1000000}; // limit of the tensor-core GEMM's bounded waits
 std::atomic<int> g_test_timeout{0};        // one-shot: the next tensor-core launch withholds a stage
+std::atomic<int> g_test_grad_timeout{0};   // one-shot: the next weight gradient withholds a stage
 std::atomic<int> g_tc_a_tmem{0};           // tensor-core GEMM with the weight operand staged in TMEM
 std::atomic<int> g_tc_form{0};             // forms of the prefill tensor-core GEMMs (MOE_OPT_TC_FORM)
 
@@ -816,7 +817,8 @@ int moe_ckpt_wgrad(const void* dy_bf16, int64_t lddy, const uint8_t* x_codes, co
         return fail(MOE_ERR_INVALID_ARG, "%s: ws_bytes %zu < %zu", who, ws_bytes,
                     moe::wgrad_workspace_bytes(R, N, K, G));
     cudaError_t e = moe::launch_ckpt_wgrad(dy_bf16, lddy, x_codes, x_scales, offsets, perm, k_div, R, X, N, K, G, dw,
-                                           accumulate, ws, load_options().wait_ns, stream);
+                                           accumulate, ws, load_options().wait_ns,
+                                           R > 0 ? g_test_grad_timeout.exchange(0) : 0, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, who);
 }
 
@@ -855,6 +857,12 @@ int moe_set_option(int option, int value) {
         g_test_timeout = value;
         return MOE_OK;
     }
+    if (option == MOE_OPT_TEST_GRAD_TIMEOUT) {
+        if (value != 0 && value != 1)
+            return fail(MOE_ERR_INVALID_ARG, "moe_set_option: TEST_GRAD_TIMEOUT must be 0 or 1");
+        g_test_grad_timeout = value;
+        return MOE_OK;
+    }
     return fail(MOE_ERR_INVALID_ARG, "moe_set_option: unknown option %d", option);
 }
 
@@ -865,6 +873,7 @@ int moe_get_option(int option) {
     if (option == MOE_OPT_TC_A_TMEM) return g_tc_a_tmem;
     if (option == MOE_OPT_TC_FORM) return g_tc_form;
     if (option == MOE_OPT_TEST_TIMEOUT) return g_test_timeout;
+    if (option == MOE_OPT_TEST_GRAD_TIMEOUT) return g_test_grad_timeout;
     return -1;
 }
 

@@ -135,6 +135,7 @@ struct GradArgs {
     BiasArgs bias;             // GM_RDW, GM_RDX
     int32_t* flag;
     uint64_t wait_ns;
+    int withhold;              // a test: the first pair's first stage is never copied
 };
 
 // ---- PTX forms of the SM pair ----------------------------------------------------
@@ -425,8 +426,10 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     auto warp_wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, !*abort && wait(bar, parity)) != 0;
     };
+    // The waits for what is in flight are not cut short: 0.1 s at the least.
+    const uint64_t drain_ns = max(a.wait_ns, (uint64_t)100000000);
     auto final_wait = [&](uint32_t bar, uint32_t parity) {
-        if (!mbar_wait_for<false>(bar, parity, a.wait_ns, nullptr)) raise_flag(a.flag, FLAG_TIMEOUT);
+        if (!mbar_wait_for<false>(bar, parity, drain_ns, nullptr)) raise_flag(a.flag, FLAG_TIMEOUT);
     };
     const Walk walk0(a, sh.rem_pre, pair, pairs);
     int stage = 0;
@@ -462,10 +465,18 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             // up: "empty" reaches both CTAs, so both have then issued the same
             // stages, and the leader's last waits cover the copies of both.)
             constexpr uint32_t bytes = (AP + BP) * GG_PLANE;
+            bool first = true;
             for (Steps s(walk0); s.on; s.advance()) {
-                if (!mbar_wait_for<false>(smem_u32(&sh.empty[stage]), phase ^ 1u, a.wait_ns, nullptr)) {
+                if (!mbar_wait_for<false>(smem_u32(&sh.empty[stage]), phase ^ 1u, drain_ns, nullptr)) {
                     give_up();
                     break;
+                }
+                if (MODE == GM_WGRAD && a.withhold) {
+                    if (pair == 0 && first) {
+                        first = false;
+                        next_stage();
+                        continue;
+                    }
                 }
                 const bool tail = has_tail(s.seg, s.st);
                 uint32_t bar = smem_u32(tail ? &sh.tail_landed[stage] : &sh.landed[stage]);
@@ -1005,7 +1016,8 @@ static cudaError_t grad_map(const void* p, CUtensorMapDataType type, long long l
     if (!encode) return cudaErrorNotSupported;
     const cuuint64_t row = (cuuint64_t)ld * (128 / box_cols);
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-    const cuuint64_t strides[2] = {row, row * (cuuint64_t)rows};
+    // (a single matrix has no plane stride to overflow)
+    const cuuint64_t strides[2] = {row, planes > 1 ? row * (cuuint64_t)rows : row};
     const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
     return encode(map, type, 3, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1097,7 +1109,7 @@ size_t router_backward_workspace_bytes(int T, int H, int E) { return router_ws(T
 
 cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* codes, const uint8_t* scales,
                               const int32_t* offsets, const int32_t* perm, int k, int R, int rows, int N, int K, int G,
-                              float* dw, int accumulate, void* ws, uint64_t wait_ns, cudaStream_t st) {
+                              float* dw, int accumulate, void* ws, uint64_t wait_ns, int withhold, cudaStream_t st) {
     int32_t* flag = (int32_t*)ws;
     cudaError_t e = cudaSuccess;
     PrepareArgs s = {};
@@ -1133,6 +1145,7 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
     a.part = (float*)((char*)ws + wgrad_part_offset(R, K));
     a.flag = flag;
     a.wait_ns = wait_ns;
+    a.withhold = withhold;
     return launch_grad<GM_WGRAD>(a, a_map, b_map, dw, st);
 }
 

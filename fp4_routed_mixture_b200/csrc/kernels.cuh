@@ -234,7 +234,7 @@ cudaError_t launch_ckpt_swiglu_backward(const uint8_t* codes, const uint8_t* sca
 size_t wgrad_workspace_bytes(int R, int N, int K, int G);
 cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* codes, const uint8_t* scales,
                               const int32_t* offsets, const int32_t* perm, int k, int R, int rows, int N, int K, int G,
-                              float* dw, int accumulate, void* ws, uint64_t wait_ns, cudaStream_t st);
+                              float* dw, int accumulate, void* ws, uint64_t wait_ns, int withhold, cudaStream_t st);
 size_t router_backward_workspace_bytes(int T, int H, int E);
 // Calls of at most kRouterGradSmallT tokens run on the CUDA cores (router_grad_small.cu).
 constexpr int kRouterGradSmallT = 64;

@@ -372,10 +372,12 @@ int moe_route_backward(const float *logits, const int32_t *topk_idx, const float
  * at least one of them.  x comes either as x_bf16 [T, H] or as an 8-bit
  * checkpoint (x_codes, x_scales, see moe_ckpt_pack; H % 128 == 0), the other
  * being NULL; neither is needed when dw is NULL.  w_router is needed for dx.
- * accumulate 1 adds dw and dbias to what is there (dx is always overwritten).
- * Products of fp32 operands are formed from exact bf16 parts, accumulated in
- * fp32: dw from all three parts of dlogits, dx from the leading two parts of
- * each operand (about 16 bits, before its rounding to 8).
+ * accumulate 1 adds dw and dbias to what is there (dx is always overwritten;
+ * sums below 2^-126 may become 0).
+ * Calls of at most 64 tokens use fp32 multiply-adds.  Larger ones form the
+ * products of fp32 operands from bf16 parts on the tensor cores, accumulated in
+ * fp32: dw from all three parts of dlogits (exact), dx from the leading two
+ * parts of each operand (about 16 bits, before its rounding to 8).
  * ws: moe_router_backward_workspace_bytes(T_max, H, E) bytes, 256-byte
  * aligned, T <= T_max; first int32: the error word, cleared by this call
  * (MOE_FLAG_TIMEOUT as in moe_forward).  H % 32 == 0, 1 <= E <= 1024; dlogits,
@@ -424,7 +426,7 @@ int moe_ckpt_swiglu_backward(const uint8_t *gu_codes, const uint8_t *gu_scales, 
  * [R] is given: with moe_sort's perm and k_div = k, dy in sorted order meets
  * the tokens' x in token order (W1); without it both are in sorted order (W2).
  * A group without rows gives 0.  Rows outside every group are not read.
- * accumulate 1 adds to what dw holds.  bf16 x bf16 products on the tensor
+ * accumulate 1 adds to what dw holds (sums below 2^-126 may become 0).  bf16 x bf16 products on the tensor
  * cores (x^ as bf16 is exact), fp32 accumulation.
  * ws: moe_ckpt_wgrad_workspace_bytes(R_max, N, K, G) bytes, 256-byte aligned,
  * R <= R_max; its first int32 is the error word, cleared by this call:
@@ -475,6 +477,9 @@ int moe_ckpt_wgrad(const void *dy_bf16, int64_t lddy, const uint8_t *x_codes, co
  *   the tensor-core W1 GEMM has its first CTA's first pipeline stage withheld
  *   (neither copied nor signalled), so the MMA waiting for it runs out of
  *   time.  The arming is consumed by that call; 0 disarms.  For tests only.
+ *   MOE_OPT_TEST_GRAD_TIMEOUT: the same test of the gradient GEMM's waits: the
+ *   next moe_ckpt_wgrad call (R > 0) has its first SM pair's first stage
+ *   withheld.  The arming is consumed by that call; 0 disarms.  For tests only.
  * moe_set_option returns MOE_OK or MOE_ERR_INVALID_ARG; moe_get_option returns
  * the current value (-1 for an unknown option). */
 #define MOE_OPT_TC_MIN_ROWS 1
@@ -483,6 +488,7 @@ int moe_ckpt_wgrad(const void *dy_bf16, int64_t lddy, const uint8_t *x_codes, co
 #define MOE_OPT_TEST_TIMEOUT 4
 #define MOE_OPT_TC_A_TMEM 5
 #define MOE_OPT_TC_FORM 6
+#define MOE_OPT_TEST_GRAD_TIMEOUT 7
 int moe_set_option(int option, int value);
 int moe_get_option(int option);
 

@@ -211,3 +211,87 @@ def test_captured_autograd_backward(moe):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_calls_allocate_nothing(moe):
+    """With outputs and workspaces given, no call allocates device memory."""
+    d = make()
+    b = buffers(moe, d)
+    step(moe, d, b)
+    torch.cuda.synchronize()
+    before, free = torch.cuda.memory_allocated(), torch.cuda.mem_get_info()[0]
+    peak = torch.cuda.max_memory_allocated()
+    for _ in range(3):
+        step(moe, d, b)
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == before and torch.cuda.max_memory_allocated() == peak
+    assert torch.cuda.mem_get_info()[0] == free
+
+
+def test_one_workspace_for_smaller_calls(moe):
+    """A workspace sized for T_max serves smaller calls, whatever an earlier call
+    left in it."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    T, H, E = 3000, 256, 40
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    dl = torch.randn(T, E, generator=g, device="cuda")
+    w = torch.randn(E, H, generator=g, device="cuda")
+    rws = torch.full((moe.moe_router_backward_workspace_bytes(T, H, E),), 0xFF, dtype=torch.uint8, device="cuda")
+    wws = torch.full((moe.moe_ckpt_wgrad_workspace_bytes(T, 64, H),), 0xFF, dtype=torch.uint8, device="cuda")
+    bws = torch.full((moe.moe_balance_workspace_bytes(T, E, 5),), 0xFF, dtype=torch.uint8, device="cuda")
+    for n in (T, 1, 70, 1500, 64, 65, 700):
+        a = moe.moe_router_logits_backward(dl[:n], w, x=x[:n], ws=rws)
+        b = moe.moe_router_logits_backward(dl[:n], w, x=x[:n])
+        for u, v in zip(a, b):
+            assert torch.equal(u, v), n
+        ck = moe.moe_ckpt_pack(x[:n])
+        dy = x[:n, :64]
+        assert torch.equal(moe.moe_ckpt_wgrad(dy, *ck, ws=wws), moe.moe_ckpt_wgrad(dy, *ck)), n
+        idx, _ = moe.moe_route(dl[:n].contiguous(), 4)
+        seq = torch.tensor([0, n // 3, n // 3, n - n // 5, n], dtype=torch.int32, device="cuda")
+        for u, v in zip(moe.moe_balance_loss(dl[:n], idx, 1.0, seq_offsets=seq, ws=bws),
+                        moe.moe_balance_loss(dl[:n], idx, 1.0, seq_offsets=seq)):
+            assert torch.equal(u, v), n
+    for ws in (rws, wws, bws):
+        assert moe.moe_check_device_flag(ws) == 0
+
+
+def test_binding_refusals(moe):
+    """Wrong types, shapes, layouts and missing parts are refused by name."""
+    d = make(T=32)
+    b = buffers(moe, d)
+    idx, gates = moe.moe_route(torch.randn(32, 24, device="cuda"), 3)
+    logits = torch.randn(32, 24, device="cuda")
+    ck = moe.moe_ckpt_pack(d["x"])
+    for call in (
+            lambda: moe.moe_balance_loss(logits.double(), idx, 0.1),
+            lambda: moe.moe_balance_loss(logits, idx.long(), 0.1),
+            lambda: moe.moe_balance_loss(logits, idx[:31], 0.1),
+            lambda: moe.moe_balance_loss(logits.t(), idx, 0.1),
+            lambda: moe.moe_balance_loss(logits, idx, 0.1, token_mask=torch.ones(31, dtype=torch.bool, device="cuda")),
+            lambda: moe.moe_balance_loss(logits, idx, 0.1, seq_offsets=torch.zeros(1, dtype=torch.int32, device="cuda")),
+            lambda: moe.moe_balance_loss(logits, idx, 0.1, seq_offsets=torch.zeros(3, dtype=torch.int32)),
+            lambda: moe.moe_balance_loss(logits, idx, 0.1, ws=torch.empty(8, dtype=torch.uint8, device="cuda")),
+            lambda: moe.moe_route_backward(logits, idx),
+            lambda: moe.moe_route_backward(logits, idx, dgates=gates),
+            lambda: moe.moe_route_backward(logits, idx, gates, dgates=gates, out=logits),
+            lambda: moe.moe_route_backward(logits, idx, dloss=torch.ones(1, device="cuda"), coef=1.0),
+            lambda: moe.moe_router_logits_backward(logits, d["wr"]),
+            lambda: moe.moe_router_logits_backward(logits, d["wr"], x=d["x"], codes=ck[0], scales=ck[1]),
+            lambda: moe.moe_router_logits_backward(logits, d["wr"], codes=ck[0]),
+            lambda: moe.moe_router_logits_backward(logits, d["wr"], x=d["x"], accumulate=True),
+            lambda: moe.moe_router_logits_backward(logits, d["wr"][:, :64], x=d["x"]),
+            lambda: moe.moe_ckpt_unpack(ck[0], ck[1][:, :1]),
+            lambda: moe.moe_ckpt_unpack(ck[0].view(torch.int8), ck[1]),
+            lambda: moe.moe_ckpt_swiglu_backward(*ck, d["dh"][:, :64]),
+            lambda: moe.moe_ckpt_swiglu_backward(*ck, d["dh"], need_h=True, out=(d["x"], None)),
+            lambda: moe.moe_ckpt_wgrad(d["dy"].float(), *ck),
+            lambda: moe.moe_ckpt_wgrad(d["dy"].t(), *ck),
+            lambda: moe.moe_ckpt_wgrad(d["dy"], ck[0][:31], ck[1][:31]),
+            lambda: moe.moe_ckpt_wgrad(d["dy"], *ck, accumulate=True),
+            lambda: moe.moe_ckpt_wgrad(d["dy"], *ck, dw=torch.empty(256, 255, device="cuda")),
+            lambda: moe.moe_ckpt_wgrad(d["dy"], *ck, perm=idx[:, 0].contiguous(), k=0),
+            lambda: moe.moe_ckpt_wgrad(d["dy"], *ck, offsets=torch.zeros(1, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(moe.MoeError):
+            call()
