@@ -31,10 +31,9 @@
 //   warps 8-15    epilogue, from two 256-column accumulators in TMEM
 // Work: pair p takes the tiles p, p + P, ... of the first floor(tiles / P) P
 // ones whole; the remaining tiles are cut so that the last round is not left to
-// a few pairs.  Where a tile has more rows than a chunk, its rows are cut into
-// chunks and dealt out evenly; the parts go to the workspace and k_grad_fixup
-// adds them in a fixed order.  Where it has fewer, storing C is what takes the
-// time (40 x 4096 x 4096: 2.6 us per tile and pair, the copy bandwidth): 2 or 4
+// a few pairs.  Where that pays, a tile's rows are cut into chunks and dealt out
+// evenly; the parts go to the workspace and k_grad_fixup adds them in a fixed
+// order.  Where a tile has few rows, storing C is what takes the time (40 x 4096 x 4096: 2.6 us per tile and pair, the copy bandwidth): 2 or 4
 // pairs compute the same tile and store a part of its columns each.
 //
 // The tensor cores truncate when they add to the fp32 accumulator, always
@@ -72,8 +71,11 @@ struct GradCfg {
     static constexpr int OPS = (AP + BP) * GG_PLANE;
     static constexpr int STAGES = MODE == GM_WGRAD ? 6 : 3;
     static constexpr int ACC_STEPS = MODE == GM_WGRAD ? 16 : MODE == GM_RDW ? 4 : 16;
-    // rows per chunk of a split tile (a result of GM_RDX has at most 16 stages and is not split)
-    static constexpr int CHUNK_STEPS = MODE == GM_WGRAD ? 16 : MODE == GM_RDW ? 8 : 16;
+    // Largest chunk of a split tile, and what splitting has to save, in stages
+    // (about 5 us, what k_grad_fixup adds: a stage takes 0.28 us in GM_WGRAD, 0.85 with
+    // three products; 512 tokens, 8 stages in 2: the same time with and without).  A result of GM_RDX, of at most 16 stages, is not split.
+    static constexpr int CHUNK_STEPS = MODE == GM_WGRAD ? 16 : 8;
+    static constexpr int SPLIT_GAIN = MODE == GM_WGRAD ? 18 : MODE == GM_RDW ? 7 : 1 << 20;
 };
 
 template <int MODE>
@@ -135,7 +137,7 @@ struct GradArgs {
     BiasArgs bias;             // GM_RDW, GM_RDX
     int32_t* flag;
     uint64_t wait_ns;
-    int withhold;              // a test: the first pair's first stage is never copied
+    int withhold;              // a test: no pair's first stage is copied
 };
 
 // ---- PTX forms of the SM pair ----------------------------------------------------
@@ -471,12 +473,10 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                     give_up();
                     break;
                 }
-                if (MODE == GM_WGRAD && a.withhold) {
-                    if (pair == 0 && first) {
-                        first = false;
-                        next_stage();
-                        continue;
-                    }
+                if (MODE == GM_WGRAD && a.withhold && first) {
+                    first = false;
+                    next_stage();
+                    continue;
                 }
                 const bool tail = has_tail(s.seg, s.st);
                 uint32_t bar = smem_u32(tail ? &sh.tail_landed[stage] : &sh.landed[stage]);
@@ -1042,11 +1042,19 @@ static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUten
     if (tiles >= (1LL << 30)) return cudaErrorInvalidValue;
     a.tiles = (int)tiles;
     a.full = a.tiles / pairs * pairs;
-    a.chunk_steps = GradCfg<MODE>::CHUNK_STEPS;
+    // The remaining tiles: chunks of rows so that every pair has one, or several of
+    // the largest size.  (The rows of a group are known on the device only: the
+    // average stands for them.)
     const int rem = a.tiles - a.full;
-    const bool split = rem > 0 && a.R > a.chunk_steps * GG_K;
+    const int max_steps = (int)(((long long)a.R + GG_K - 1) / GG_K);
+    const int steps = (int)(((long long)a.R / a.G + GG_K - 1) / GG_K);
+    const int per = rem > 0 ? pairs / rem : 1;
+    a.chunk_steps = std::max(1, std::min((steps + per - 1) / per, GradCfg<MODE>::CHUNK_STEPS));
+    const int longest = (int)(((long long)rem * ((steps + a.chunk_steps - 1) / a.chunk_steps) + pairs - 1) / pairs) * a.chunk_steps;
+    const bool split = rem > 0 && steps - longest >= GradCfg<MODE>::SPLIT_GAIN;
+    if (!split) a.chunk_steps = std::max(1, max_steps);
     // (4 ways: 64 columns, the narrowest store of GM_RDX)
-    a.ways = split || rem == 0 ? 1 : pairs >= 4 * rem ? 4 : pairs >= 2 * rem ? 2 : 1;
+    a.ways = split || rem == 0 ? 1 : per >= 4 ? 4 : per >= 2 ? 2 : 1;
     CUtensorMap c_map, part_map;
     cudaError_t e;
     if (MODE == GM_RDX)
@@ -1081,13 +1089,13 @@ static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUten
 }
 
 // Workspace: the error word (256 bytes), the operands as bf16, the parts of
-// split tiles (where a tile can be split: more rows than one chunk).
-static size_t grad_part_bytes(int R, int chunk_steps) {
-    return R > chunk_steps * GG_K ? (size_t)GG_MAX_PAIRS * 2 * GG_TILE * GG_TILE * sizeof(float) : 0;
+// split tiles (where a tile can be split).
+static size_t grad_part_bytes(int R, int split_gain) {
+    return R > split_gain * GG_K ? (size_t)GG_MAX_PAIRS * 2 * GG_TILE * GG_TILE * sizeof(float) : 0;
 }
 static size_t wgrad_part_offset(int R, int K) { return 256 + align_up(2 * (size_t)R * K, 256); }
 size_t wgrad_workspace_bytes(int R, int, int K, int) {
-    return wgrad_part_offset(R, K) + grad_part_bytes(R, GradCfg<GM_WGRAD>::CHUNK_STEPS);
+    return wgrad_part_offset(R, K) + grad_part_bytes(R, GradCfg<GM_WGRAD>::SPLIT_GAIN);
 }
 
 struct RouterWs {
@@ -1101,7 +1109,7 @@ static RouterWs router_ws(int T, int H, int E) {
     L.bias = o; o += align_up(sizeof(float) * kSplitMaxCtas * (size_t)E, 256);
     L.dlp = o; o += align_up(3 * 2 * (size_t)T * Ep, 256);
     L.xb = o; o += align_up(2 * (size_t)T * H, 256);
-    L.part = o; o += grad_part_bytes(T, GradCfg<GM_RDW>::CHUNK_STEPS);
+    L.part = o; o += grad_part_bytes(T, GradCfg<GM_RDW>::SPLIT_GAIN);
     L.total = o;
     return L;
 }

@@ -478,8 +478,7 @@ int moe_ckpt_wgrad(const void *dy_bf16, int64_t lddy, const uint8_t *x_codes, co
  *   (neither copied nor signalled), so the MMA waiting for it runs out of
  *   time.  The arming is consumed by that call; 0 disarms.  For tests only.
  *   MOE_OPT_TEST_GRAD_TIMEOUT: the same test of the gradient GEMM's waits: the
- *   next moe_ckpt_wgrad call (R > 0) has its first SM pair's first stage
- *   withheld.  The arming is consumed by that call; 0 disarms.  For tests only.
+ *   next moe_ckpt_wgrad call (R > 0) has each SM pair's first stage withheld.  The arming is consumed by that call; 0 disarms.  For tests only.
  * moe_set_option returns MOE_OK or MOE_ERR_INVALID_ARG; moe_get_option returns
  * the current value (-1 for an unknown option). */
 #define MOE_OPT_TC_MIN_ROWS 1

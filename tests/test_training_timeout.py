@@ -1,7 +1,7 @@
 """The gradient GEMM's bounded waits, made to run out on purpose.
 
-MOE_OPT_TEST_GRAD_TIMEOUT makes the next weight gradient withhold its first SM
-pair's first stage (no copy and no arrival: a barrier that nothing completes);
+MOE_OPT_TEST_GRAD_TIMEOUT makes the next weight gradient withhold each SM pair's
+first stage (no copy and no arrival: a barrier that nothing completes);
 with a short limit the wait ends in milliseconds.  The call must raise
 MOE_FLAG_TIMEOUT and return, and the next call in the same process be exact.
 Nothing faults, traps or hangs.
