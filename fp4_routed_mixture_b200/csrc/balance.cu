@@ -169,7 +169,10 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_rows(BalanceArgs a) {
     for (int s = ONE ? 0 : a.seq.find(r0); s < a.seq.S; ++s) {
         if (!ONE && a.seq.at(s) >= r1) break;
         const int b = max(a.seq.at(s), r0), e = min(a.seq.at(s + 1), r1);
-        if (!ONE && e <= b) continue;
+        if (!ONE && e <= b) {
+            s = max(s, a.seq.find(b) - 1);       // (past a run of empty ones)
+            continue;
+        }
         for (int c = threadIdx.x; c < a.E; c += kBalThreads) sc[c] = 0;
         if (threadIdx.x == 0) s_n = s_bad = 0;
         __syncthreads();

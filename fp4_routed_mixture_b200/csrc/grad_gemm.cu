@@ -75,7 +75,7 @@ struct GradCfg {
     // (about 5 us, what k_grad_fixup adds: a stage takes 0.28 us in GM_WGRAD, 0.85 with
     // three products; 512 tokens, 8 stages in 2: the same time with and without).  A result of GM_RDX, of at most 16 stages, is not split.
     static constexpr int CHUNK_STEPS = MODE == GM_WGRAD ? 16 : 8;
-    static constexpr int SPLIT_GAIN = MODE == GM_WGRAD ? 18 : MODE == GM_RDW ? 7 : 1 << 20;
+    static constexpr int SPLIT_GAIN = MODE == GM_WGRAD ? 18 : MODE == GM_RDW ? 8 : 1 << 20;
 };
 
 template <int MODE>
@@ -582,7 +582,12 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         } else if (MODE == GM_WGRAD && warp == 2 && a.perm) {
             // (k_grad_prepare reads row 0 for a bad entry; the error word is this
             // call's only from the second kernel on)
-            for (long long i = blockIdx.x * 32 + lane; i < a.R; i += gridDim.x * 32) {
+            int r0 = 0, r1 = a.R, unused;
+            if (a.offsets) {
+                gg_rows(a, 0, r0, unused);
+                gg_rows(a, a.G - 1, unused, r1);
+            }
+            for (long long i = (long long)r0 + blockIdx.x * 32 + lane; i < r1; i += gridDim.x * 32) {
                 const int v = __ldg(a.perm + i);
                 checked_index(v < 0 ? v : v / a.k_div, a.xrows, a.flag);
             }

@@ -425,7 +425,8 @@ int moe_ckpt_swiglu_backward(const uint8_t *gu_codes, const uint8_t *gu_scales, 
  * with x^ the restored checkpoint and row(i) = i, or perm[i] / k_div when perm
  * [R] is given: with moe_sort's perm and k_div = k, dy in sorted order meets
  * the tokens' x in token order (W1); without it both are in sorted order (W2).
- * A group without rows gives 0.  Rows outside every group are not read.
+ * A group without rows gives 0.  Rows outside every group (and their perm
+ * entries) take no part.
  * accumulate 1 adds to what dw holds (sums below 2^-126 may become 0).  bf16 x bf16 products on the tensor
  * cores (x^ as bf16 is exact), fp32 accumulation.
  * ws: moe_ckpt_wgrad_workspace_bytes(R_max, N, K, G) bytes, 256-byte aligned,

@@ -107,6 +107,28 @@ def test_balance_loss_and_gradient(moe, T, E, k, seq, masked):
         assert moe.moe_check_device_flag(ws) == 0
 
 
+def test_balance_many_sequences(moe):
+    """More sequences than rows, runs of empty ones, the last rows in none."""
+    T, E, k, S = 3000, 24, 3, 5000
+    logits, idx, gates, dgates = routed(T, E, k, 3)
+    r = np.random.default_rng(1)
+    seq = np.sort(r.integers(0, T - 20, S + 1)).astype(np.int32)
+    seq[1000:3000] = seq[1000]
+    kw = dict(seq_offsets=cu(seq))
+    ws = torch.zeros(moe.moe_balance_workspace_bytes(T, E, S), dtype=torch.uint8, device="cuda")
+    loss, counts, prob, tokens = moe.moe_balance_loss(cu(logits), cu(idx), 1.0, ws=ws, **kw)
+    assert moe.moe_check_device_flag(ws) == 0
+    rl, rc, rp, rt = ref.balance(logits, idx, 1.0, seq)
+    assert np.array_equal(host(counts), rc) and np.array_equal(host(tokens), rt)
+    rel = rel_softmax(logits) + (T + 40) * U
+    close(host(prob), rp, rel * rp, "mean_prob")
+    close(host(loss), [rl], (rel + 8 * U) * abs(rl), "loss")
+    d = moe.moe_route_backward(cu(logits), cu(idx), dloss=torch.ones(1, device="cuda"), coef=1.0, counts=counts,
+                               tokens=tokens, **kw)
+    want, size = ref.route_backward(logits, idx, None, None, 1.0, 1.0, seq)
+    close(host(d), want, (rel_softmax(logits) + 30 * U) * size, "dlogits")
+
+
 def test_balance_gradient_against_differences(moe):
     """The loss's slope along a direction, from the loss itself (the counts are
     constants): central differences of the 64-bit definition."""
@@ -207,6 +229,10 @@ def pow2_rows(x):
     (1, 128, 1, "ckpt"), (1, 32, 3, "bf16"), (5, 96, 7, "bf16"), (64, 256, 16, "ckpt"), (63, 128, 65, "ckpt"),
     (130, 512, 256, "ckpt"), (257, 288, 100, "bf16"), (40, 4096, 256, "bf16"), (1000, 256, 33, "ckpt"),
     (129, 384, 1024, "ckpt"), (70, 160, 1023, "bf16"), (2500, 640, 8, "ckpt"), (333, 1056, 260, "bf16"),
+    # either side of the rule on the number of tokens, with the smallest and odd sizes
+    (65, 32, 1, "bf16"), (300, 128, 1, "ckpt"), (66, 96, 3, "bf16"), (100, 32, 7, "bf16"), (65, 128, 65, "ckpt"),
+    (64, 160, 1023, "bf16"), (31, 32, 1024, "bf16"), (33, 640, 130, "ckpt"), (1, 4096, 2, "bf16"),
+    (1500, 256, 5, "bf16"), (1100, 512, 513, "ckpt"),
 ])
 def test_router_backward(moe, T, H, E, kind):
     r = np.random.default_rng(T + H + E)
@@ -509,3 +535,60 @@ def test_wgrad_exponent_range(moe):
     close(dw[:, 128:], (dy.T @ x)[:, 128:], wgrad_bound(dy, x)[:, 128:], "large")
     # sums below fp32's normal range may be flushed
     close(dw[:, :128], (dy.T @ x)[:, :128], wgrad_bound(dy, x)[:, :128] + R * 2.0 ** -126, "small")
+
+
+def test_wgrad_rows_behind_the_last_group_take_no_part(moe):
+    """A sort that left pairs out: rows and table entries behind the last group."""
+    R, N, K, k = 200, 64, 128, 2
+    codes, scales, dyb, x, dy = wgrad_case(moe, R // k, R, N, K, 77)
+    perm = np.random.default_rng(0).permutation(R).astype(np.int32)
+    off = np.array([0, 70, 131], np.int32)
+    bad = perm.copy()
+    bad[131:] = -12345
+    ws = torch.zeros(moe.moe_ckpt_wgrad_workspace_bytes(R, N, K, 2), dtype=torch.uint8, device="cuda")
+    got = host(moe.moe_ckpt_wgrad(dyb, codes, scales, offsets=cu(off), perm=cu(bad), k=k, ws=ws))
+    assert moe.moe_check_device_flag(ws) == 0
+    for g in range(2):
+        rows = np.arange(off[g], off[g + 1])
+        close(got[g], dy[rows].T @ x[perm[rows] // k], wgrad_bound(dy[rows], x[perm[rows] // k]), f"dw[{g}]")
+    bad[3] = -1
+    moe.moe_ckpt_wgrad(dyb, codes, scales, offsets=cu(off), perm=cu(bad), k=k, ws=ws)
+    assert moe.moe_check_device_flag(ws) == moe.FLAG_BOUNDS
+
+
+# ---- offsets beyond 32 bits -----------------------------------------------------------------
+
+def test_element_offsets_beyond_32_bits(moe):
+    """The last rows of tensors of more than 2^31 elements are those of the rows
+    alone, and the sum over all rows is that of its parts."""
+    T, K = 530000, 4096                       # 2.17e9 elements
+    x = torch.empty((T, K), dtype=torch.bfloat16, device="cuda").normal_()
+    codes, scales = moe.moe_ckpt_pack(x)
+    c, s = moe.moe_ckpt_pack(x[-3:].clone())
+    assert torch.equal(codes[-3:], c) and torch.equal(scales[-3:], s)
+    moe.moe_ckpt_unpack(codes, scales, out=x)
+    assert torch.equal(x[-3:], moe.moe_ckpt_unpack(c, s))
+    dgu, h = moe.moe_ckpt_swiglu_backward(codes, scales, x[:, :K // 2], need_h=True)
+    d2, h2 = moe.moe_ckpt_swiglu_backward(c, s, x[-3:, :K // 2])
+    assert torch.equal(dgu[-3:], d2)
+    del dgu, h, d2
+    dy = x[:, 128:136]
+    whole = moe.moe_ckpt_wgrad(dy, codes, scales).double()
+    parts = sum(moe.moe_ckpt_wgrad(dy[a:b], codes[a:b], scales[a:b]).double()
+                for a, b in ((0, T // 3), (T // 3, T - 7), (T - 7, T)))
+    # two sums of T terms, drained every 1024 rows (64 truncations) into fp32
+    size = float((dy.double() ** 2).sum(0).max().sqrt()) * float((x.double()[:, 0] ** 2).sum().sqrt())
+    assert float((whole - parts).abs().max()) <= 2 * (64 * 2 * U + T / 1024 * U) * size
+    del x, codes, scales, dy, whole, parts
+    T, E, k = 2200000, 1000, 2                # 2.2e9 logits
+    z = torch.empty((T, E), device="cuda").normal_()
+    idx = torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda")
+    gates = torch.rand((T, k), device="cuda")
+    d = moe.moe_route_backward(z, idx, gates, dgates=gates)
+    assert torch.equal(d[-5:], moe.moe_route_backward(z[-5:].clone(), idx[-5:], gates[-5:], dgates=gates[-5:]))
+    del d
+    seq = torch.tensor([0, T - 5, T], dtype=torch.int32, device="cuda")
+    _, counts, prob, tokens = moe.moe_balance_loss(z, idx, 1.0, seq_offsets=seq)
+    _, c1, p1, _ = moe.moe_balance_loss(z[-5:].clone(), idx[-5:], 1.0)
+    assert torch.equal(counts[1], c1[0]) and torch.allclose(prob[1], p1[0], rtol=1e-5, atol=0)
+    assert tokens.tolist() == [T - 5, 5, 2]
