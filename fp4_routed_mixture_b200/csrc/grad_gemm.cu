@@ -61,7 +61,7 @@ constexpr int GG_OUT = 32 * 128;
 constexpr int GG_MAX_PAIRS = 128;
 // Registers per thread: at launch, and of the two kinds of warpgroup after
 // setmaxnreg.  The epilogue holds 128 sums per thread.
-constexpr int GG_REGS = 128, GG_REGS_LOAD = 88, GG_REGS_EPI = 168;
+constexpr int GG_REGS = 128, GG_REGS_LOAD = 64, GG_REGS_EPI = 192;
 static_assert(2 * GG_REGS_LOAD + 2 * GG_REGS_EPI <= 4 * GG_REGS, "registers of the block");
 
 template <int MODE>
@@ -197,10 +197,9 @@ __device__ __forceinline__ void gg_tma_store(const CUtensorMap* map, int x, int 
                      : "memory");
 }
 // Bounded wait on a phase of an mbarrier (see mbar_wait_for), the thread asleep
-// for up to 20 us per try: without the hint a try returns at once, and the
-// waiting roles' polling was three quarters of the instructions and 4 percent of
-// the time under the power limit (16384 x 4096 x 4096, 495 -> 475 us in a loop of
-// seconds).
+// for up to 20 us per try.  (Without that hint the waiting roles' polling was
+// most of the instructions executed and cost 5 percent under the power limit:
+// 16384 x 4096 x 4096 in a loop of seconds, 495 us against 469.)
 __device__ __forceinline__ bool gg_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int32_t* abort) {
     auto poll = [&]() {
         uint32_t ok;
@@ -233,6 +232,16 @@ __device__ __forceinline__ void gg_fence_async() { asm volatile("fence.proxy.asy
 __device__ __forceinline__ void gg_st16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
+}
+// Two sums at once (Blackwell's packed fp32 addition, round to nearest).
+__device__ __forceinline__ void gg_add2(float& a, float& b, uint32_t u, uint32_t v) {
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%0, %1};\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "add.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(u), "r"(v));
 }
 // 32 lanes x 16 columns: lane = row.
 __device__ __forceinline__ void gg_ld32x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                     gg_ld32x16(tmem + ((uint32_t)(32 * q) << 16) + buf * GG_TILE + 128 * half + 16 * i, v);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][e] = __fadd_rn(acc[i][e], __uint_as_float(v[e]));
+                    for (int e = 0; e < 16; e += 2) gg_add2(acc[i][e], acc[i][e + 1], v[e], v[e + 1]);
                 }
                 tc_fence_before();
                 __syncwarp();
