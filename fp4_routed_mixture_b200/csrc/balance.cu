@@ -62,12 +62,18 @@ struct SeqTable {
         if (!off) return s == 0 ? 0 : T;
         return min(max(__ldg(off + s), 0), T);
     }
-    // the first sequence that ends behind row r (S when none does)
+    // The first sequence that ends behind row r (S when none does); by a whole
+    // warp, 32 bounds at a time (one after the other they cost 0.6 us each).
     __device__ int find(int r) const {
-        int lo = 0, hi = S;
+        const int lane = threadIdx.x & 31;
+        int lo = 0, hi = S;                  // the answer lies in [lo, hi]
         while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (at(mid + 1) > r) hi = mid; else lo = mid + 1;
+            const int step = (hi - lo + 31) / 32, s = min(lo + (lane + 1) * step - 1, hi - 1);
+            const uint32_t m = __ballot_sync(0xffffffffu, at(s + 1) > r);
+            if (m == 0) return hi;
+            const int first = __ffs((int)m) - 1;
+            hi = min(lo + (first + 1) * step - 1, hi - 1);
+            lo += first * step;
         }
         return lo;
     }
@@ -178,16 +184,22 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_rows(BalanceArgs a) {
         __syncthreads();
         float acc[N] = {};
         float nx[N];
-        if (b + warp < e) load_row<N, VEC>(a.logits + (size_t)(b + warp) * a.E, a.E, lane, nx);
+        int nid = -1, non = 1;
+        // a row's logits, ids and mask are loaded one row ahead
+        auto fetch = [&](int r) {
+            load_row<N, VEC>(a.logits + (size_t)r * a.E, a.E, lane, nx);
+            if (lane < a.k) nid = __ldg(a.idx + (size_t)r * a.k + lane);
+            if (a.mask) non = __ldg(a.mask + r);
+        };
+        if (b + warp < e) fetch(b + warp);
         int n = 0;
         for (int r = b + warp; r < e; r += kBalWarps) {
             float x[N];
 #pragma unroll
             for (int v = 0; v < N; ++v) x[v] = nx[v];
-            int id = -1;
-            const bool on = !(a.mask && !__ldg(a.mask + r));
-            if (on && lane < a.k) id = __ldg(a.idx + (size_t)r * a.k + lane);
-            if (r + kBalWarps < e) load_row<N, VEC>(a.logits + (size_t)(r + kBalWarps) * a.E, a.E, lane, nx);
+            const int id = nid;
+            const bool on = non != 0;
+            if (r + kBalWarps < e) fetch(r + kBalWarps);
             if (!on) continue;
             ++n;
             const float inv = row_inverse(warp_sum(row_exp<N>(x)));
@@ -386,21 +398,28 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(RouteBackwardA
     const int r0 = (int)first, r1 = (int)min((long long)a.T, first + a.rows);
     int s = -1, s_end = r0;       // the sequence whose f is in registers ends at s_end
     float f[N], w = 0.0f;
-    float nx[N];
-    load_row<N, VEC>(a.logits + (size_t)r0 * a.E, a.E, lane, nx);
+    float nx[N], ng = 0.0f, ndg = 0.0f;
+    int nid = -1, non = 1;
+    // what a row needs is loaded one row ahead
+    auto fetch = [&](int r) {
+        load_row<N, VEC>(a.logits + (size_t)r * a.E, a.E, lane, nx);
+        if (a.dgates && lane < a.k) {
+            const size_t at = (size_t)r * a.k + lane;
+            nid = __ldg(a.idx + at);
+            ng = __ldg(a.gates + at);
+            ndg = __ldg(a.dgates + at);
+        }
+        if (a.mask) non = __ldg(a.mask + r);
+    };
+    fetch(r0);
     for (int r = r0; r < r1; ++r) {
         float x[N];
 #pragma unroll
         for (int v = 0; v < N; ++v) x[v] = nx[v];
-        float g = 0.0f, dg = 0.0f;
-        int id = -1;
-        if (a.dgates && lane < a.k) {
-            id = __ldg(a.idx + (size_t)r * a.k + lane);
-            g = __ldg(a.gates + (size_t)r * a.k + lane);
-            dg = __ldg(a.dgates + (size_t)r * a.k + lane);
-        }
-        if (r + 1 < r1) load_row<N, VEC>(a.logits + (size_t)(r + 1) * a.E, a.E, lane, nx);
-        const bool on = a.dloss && !(a.mask && !__ldg(a.mask + r));
+        const float g = ng, dg = ndg;
+        const int id = nid;
+        const bool on = a.dloss && non;
+        if (r + 1 < r1) fetch(r + 1);
         if (on && r >= s_end) {
             s = a.seq.find(r);
             s_end = s < a.seq.S ? a.seq.at(s + 1) : a.T;
