@@ -12,9 +12,12 @@
 // A chunk c of rows and a sequence s that meet own slot c + s of the
 // workspace: walking the rows, every step to the next (chunk, sequence) pair
 // raises c, s or both, so the sum is unique, and chunks + S slots are enough
-// for any ragged split.  No atomics on floating-point values: results do not
+// for any ragged split.  No two additions to one address race: results do not
 // depend on the order in which CTAs run.
-// All three read [T, E] once (the backward also writes it): HBM bound.
+// All three read [T, E] once (the backward also writes it): HBM bound when T is
+// large.  One B200, 65536 x 256 logits in 16 sequences: loss 21 us (3.2 TB/s; a
+// warp's row is short, and two rows per warp, other block sizes and more blocks
+// measured 17 to 25 us for the rows but no less in all), gradient 28 us.
 #include "kernels.cuh"
 #include "moe_common.cuh"
 
@@ -385,8 +388,8 @@ struct RouteBackwardArgs {
 // only through sum e and sum e f (e = exp(x - max)), reduced together.  The
 // gates' terms are added to the stored row in memory: comparing each of the k
 // ids with a lane's columns in registers took two thirds of the instructions.
-// 65536 x 256 logits: 25 us (134 MB, 5.4 TB/s), 31 us with 6 gates a row; the
-// terms through shared memory 38 us, two or three rows loaded ahead 42 us.
+// 65536 x 256 logits: 25 us (134 MB, 5.4 TB/s), 28 us with 6 gates a row; the
+// terms through shared memory 7 us more, two or three rows loaded ahead 9.
 constexpr int kRouteThreads = 256, kRouteWarps = kRouteThreads / 32;
 
 template <int N, bool VEC>

@@ -1,5 +1,7 @@
 // 8-bit activation checkpoints (format: ckpt.cuh) and the SwiGLU gradient that
-// reads its inputs from one.  All three kernels stream: HBM bound.
+// reads its inputs from one.  All three kernels stream: HBM bound.  One B200,
+// 16384 rows: store 33 us and restore 31 us of 4096 values (201 MB each, 6.1 and
+// 6.5 TB/s), SwiGLU gradient of 2048 with h 56 us (336 MB, 6.0 TB/s).
 #include "ckpt.cuh"
 #include "kernels.cuh"
 #include "moe_common.cuh"

@@ -8,7 +8,8 @@
 // dbias), the others dx in tiles of 32 tokens x 32 columns, four groups of
 // threads a quarter of the experts each.  Each CTA has one round of loads (per
 // 256 experts of dx) and then computes from shared memory, 16 multiply-adds for
-// two or four 16-byte reads.
+// two 16-byte reads.  One B200, 256 experts, H = 4096: 11.7 us for 64 tokens, 7.2
+// for one; the tensor-core form 21.7 and 21.9 (65 tokens: 22.8).
 #include "ckpt.cuh"
 #include "kernels.cuh"
 #include "moe_common.cuh"

@@ -361,6 +361,12 @@ def test_ckpt_strided_rows(moe):
         moe.moe_ckpt_pack(wide.float())
 
 
+def test_ckpt_no_rows(moe):
+    codes, scales = moe.moe_ckpt_pack(torch.empty((0, 256), dtype=torch.bfloat16, device="cuda"))
+    assert codes.shape == (0, 256) and scales.shape == (0, 2)
+    assert moe.moe_ckpt_unpack(codes, scales).shape == (0, 256)
+
+
 def test_ckpt_nan_scale_byte(moe):
     codes = torch.full((2, 256), 0x38, dtype=torch.uint8, device="cuda")
     scales = torch.tensor([[127, 255], [0, 254]], dtype=torch.uint8, device="cuda")

@@ -81,7 +81,8 @@ def ckpt_value(codes, scales):
 def ckpt_pack(x):
     """Codes and scales of x [T, K] (float values of bf16 numbers)."""
     T, K = x.shape
-    b = x.astype(np.float64).reshape(T, K // 128, 128)
+    with np.errstate(invalid="ignore"):          # (signalling NaNs)
+        b = x.astype(np.float64).reshape(T, K // 128, 128)
     fin = np.isfinite(b)
     a = np.where(fin, np.abs(b), 0.0).max(axis=2)
     e = np.full(a.shape, -127, int)
