@@ -1215,7 +1215,7 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
         if (e == cudaSuccess && db && !accumulate) e = cudaMemsetAsync(db, 0, sizeof(float) * E, st);
         return e;
     }
-    if (T <= kRouterGradSmallT)
+    if (router_grad_small(T, H, E))
         return launch_router_grad_small(dl, x, codes, scales, w, T, H, E, dx, dw, db, accumulate, flag, st);
     const RouterWs L = router_ws(T, H, E);
     char* b = (char*)ws;

@@ -1,23 +1,23 @@
-// Gradients of the router projection for few tokens (T <= kRouterGradSmallT),
-// in one launch on the CUDA cores:
+// Gradients of the router projection for few tokens (router_grad_small in
+// kernels.cuh says which calls), in one launch on the CUDA cores:
 //   dw[e, h] = sum_t dl[t, e] x[t, h],  dx[t, h] = sum_e dl[t, e] w[e, h],
 //   dbias[e] = sum_t dl[t, e]
 // with fp32 fused multiply-adds in a fixed order.  The tensor-core form
 // (grad_gemm.cu) takes three launches, each of them mostly latency at these
 // sizes.  The grid's first CTAs take dw in tiles of 64 experts x 64 columns (and
-// dbias), the others dx in tiles of 32 tokens x 32 columns, four groups of
-// threads a quarter of the experts each.  Each CTA has one round of loads (per
-// 256 experts of dx) and then computes from shared memory, 16 multiply-adds for
-// two 16-byte reads.  One B200, 256 experts, H = 4096: 11.7 us for 64 tokens, 7.2
-// for one; the tensor-core form 21.7 and 21.9 (65 tokens: 22.8).
+// dbias), 64 tokens a round, the others dx in tiles of 32 tokens x 32 columns, 256
+// experts a round, four groups of threads a quarter of them each.  A round's loads
+// are issued together (dw's next ones before this one's products); the products
+// read shared memory, 16 multiply-adds for two 16-byte reads.
+// One B200, 256 experts, H = 4096: 11.7 us for 64 tokens, 7.2 for one.
 #include "ckpt.cuh"
 #include "kernels.cuh"
 #include "moe_common.cuh"
 
 namespace moe {
 
-constexpr int RS_T = kRouterGradSmallT, RS_THREADS = 256;
-constexpr int RS_WE = 64, RS_WH = 64;                 // tile of dw
+constexpr int RS_THREADS = 256;
+constexpr int RS_WE = 64, RS_WH = 64, RS_T = 64;      // tile of dw, tokens per round
 constexpr int RS_XT = 32, RS_XH = 32, RS_XE = 256;    // tile of dx, experts per round
 
 struct RouterSmallArgs {
@@ -70,70 +70,81 @@ __global__ void __launch_bounds__(RS_THREADS) k_router_grad_small(RouterSmallArg
         const int e0 = RS_WE * ((int)blockIdx.x / a.w_cols), h0 = RS_WH * ((int)blockIdx.x % a.w_cols);
         const bool vec = (a.E & 3) == 0;
         constexpr int ND = RS_T * (RS_WE / 4) / RS_THREADS, NX = RS_T * (RS_WH / 8) / RS_THREADS;
+        // experts 4 (tid / 16) .. + 3, columns 4 (tid % 16) .. + 3
+        const int me = 4 * (tid >> 4), mc = 4 * (tid & 15);
+        const bool sums = a.db && h0 == 0 && tid < RS_WE && e0 + tid < a.E;
+        float acc[4][4] = {}, bias = 0.0f;
         float4 d[ND];
         uint4 xq[NX];
         uint32_t xf[NX];
+        auto fetch = [&](int t0) {
 #pragma unroll
-        for (int u = 0; u < ND; ++u) {
-            const int i = tid + u * RS_THREADS, t = i / (RS_WE / 4), e = 4 * (i % (RS_WE / 4));
-            d[u] = rs_load4(a.dl + (size_t)t * a.E + e0 + e, t < a.T ? a.E - e0 - e : 0, vec);
-        }
+            for (int u = 0; u < ND; ++u) {
+                const int i = tid + u * RS_THREADS, t = t0 + i / (RS_WE / 4), e = 4 * (i % (RS_WE / 4));
+                d[u] = rs_load4(a.dl + (size_t)t * a.E + e0 + e, t < a.T ? a.E - e0 - e : 0, vec);
+            }
 #pragma unroll
-        for (int u = 0; u < NX; ++u) {
-            const int i = tid + u * RS_THREADS, t = i / (RS_WH / 8), c = 8 * (i % (RS_WH / 8));
-            xq[u] = make_uint4(0u, 0u, 0u, 0u);
-            xf[u] = 0u;
-            if (a.dw && t < a.T && h0 + c < a.H) {
-                const size_t at = (size_t)t * a.H + h0 + c;
-                if (a.x) {
-                    xq[u] = __ldg(reinterpret_cast<const uint4*>(a.x + at));
-                } else {
-                    const uint2 q = __ldg(reinterpret_cast<const uint2*>(a.codes + at));
-                    xq[u].x = q.x;
-                    xq[u].y = q.y;
-                    xf[u] = __ldg(a.scales + (at >> 7));
+            for (int u = 0; u < NX; ++u) {
+                const int i = tid + u * RS_THREADS, t = t0 + i / (RS_WH / 8), c = 8 * (i % (RS_WH / 8));
+                xq[u] = make_uint4(0u, 0u, 0u, 0u);
+                xf[u] = 0u;
+                if (a.dw && t < a.T && h0 + c < a.H) {
+                    const size_t at = (size_t)t * a.H + h0 + c;
+                    if (a.x) {
+                        xq[u] = __ldg(reinterpret_cast<const uint4*>(a.x + at));
+                    } else {
+                        const uint2 q = __ldg(reinterpret_cast<const uint2*>(a.codes + at));
+                        xq[u].x = q.x;
+                        xq[u].y = q.y;
+                        xf[u] = __ldg(a.scales + (at >> 7));
+                    }
                 }
             }
-        }
+        };
+        fetch(0);
+        for (int t0 = 0; t0 < a.T; t0 += RS_T) {
+            if (t0) __syncthreads();
 #pragma unroll
-        for (int u = 0; u < ND; ++u) {
-            const int i = tid + u * RS_THREADS;
-            *reinterpret_cast<float4*>(&s.d[i / (RS_WE / 4)][4 * (i % (RS_WE / 4))]) = d[u];
-        }
+            for (int u = 0; u < ND; ++u) {
+                const int i = tid + u * RS_THREADS;
+                *reinterpret_cast<float4*>(&s.d[i / (RS_WE / 4)][4 * (i % (RS_WE / 4))]) = d[u];
+            }
 #pragma unroll
-        for (int u = 0; u < NX; ++u) {
-            const int i = tid + u * RS_THREADS, t = i / (RS_WH / 8), c = 8 * (i % (RS_WH / 8));
-            float v[8];
-            if (a.x)
-                bf16x8_values(xq[u], v);
-            else
-                ckpt_values8(make_uint2(xq[u].x, xq[u].y), ckpt_scale(xf[u]), v);
-            *reinterpret_cast<float4*>(&s.x[t][c]) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(&s.x[t][c + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+            for (int u = 0; u < NX; ++u) {
+                const int i = tid + u * RS_THREADS, t = i / (RS_WH / 8), c = 8 * (i % (RS_WH / 8));
+                float v[8];
+                if (a.x)
+                    bf16x8_values(xq[u], v);
+                else
+                    ckpt_values8(make_uint2(xq[u].x, xq[u].y), ckpt_scale(xf[u]), v);
+                *reinterpret_cast<float4*>(&s.x[t][c]) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4*>(&s.x[t][c + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+            }
+            __syncthreads();
+            const int n = min(RS_T, a.T - t0);
+            if (t0 + RS_T < a.T) fetch(t0 + RS_T);       // (in flight during the products)
+            if (sums)
+                for (int t = 0; t < n; ++t) bias += s.d[t][tid];
+            if (a.dw)
+#pragma unroll 8
+                for (int t = 0; t < n; ++t) {
+                    const float4 dl = *reinterpret_cast<const float4*>(&s.d[t][me]);
+                    const float4 v = *reinterpret_cast<const float4*>(&s.x[t][mc]);
+                    const float dv[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[i][0] = fmaf(dv[i], v.x, acc[i][0]);
+                        acc[i][1] = fmaf(dv[i], v.y, acc[i][1]);
+                        acc[i][2] = fmaf(dv[i], v.z, acc[i][2]);
+                        acc[i][3] = fmaf(dv[i], v.w, acc[i][3]);
+                    }
+                }
         }
-        __syncthreads();
-        if (a.db && h0 == 0 && tid < RS_WE && e0 + tid < a.E) {
-            float v = 0.0f;
-            for (int t = 0; t < a.T; ++t) v += s.d[t][tid];
+        if (sums) {
             float* o = a.db + e0 + tid;
-            *o = a.accumulate ? *o + v : v;
+            *o = a.accumulate ? *o + bias : bias;
         }
         if (!a.dw) return;
-        // experts 4 (tid / 16) .. + 3, columns 4 (tid % 16) .. + 3
-        const int me = 4 * (tid >> 4), mc = 4 * (tid & 15);
-        float acc[4][4] = {};
-#pragma unroll 8
-        for (int t = 0; t < a.T; ++t) {
-            const float4 d = *reinterpret_cast<const float4*>(&s.d[t][me]), v = *reinterpret_cast<const float4*>(&s.x[t][mc]);
-            const float dv[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[i][0] = fmaf(dv[i], v.x, acc[i][0]);
-                acc[i][1] = fmaf(dv[i], v.y, acc[i][1]);
-                acc[i][2] = fmaf(dv[i], v.z, acc[i][2]);
-                acc[i][3] = fmaf(dv[i], v.w, acc[i][3]);
-            }
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (e0 + me + i < a.E && h0 + mc < a.H) {

@@ -233,6 +233,8 @@ def pow2_rows(x):
     (65, 32, 1, "bf16"), (300, 128, 1, "ckpt"), (66, 96, 3, "bf16"), (100, 32, 7, "bf16"), (65, 128, 65, "ckpt"),
     (64, 160, 1023, "bf16"), (31, 32, 1024, "bf16"), (33, 640, 130, "ckpt"), (1, 4096, 2, "bf16"),
     (1500, 256, 5, "bf16"), (1100, 512, 513, "ckpt"),
+    (128, 96, 70, "bf16"), (129, 2048, 600, "bf16"), (256, 1024, 512, "ckpt"), (256, 1056, 512, "bf16"),
+    (257, 32, 1, "bf16"), (300, 96, 3, "bf16"), (290, 32, 7, "bf16"), (320, 128, 65, "ckpt"), (200, 256, 100, "ckpt"),
 ])
 def test_router_backward(moe, T, H, E, kind):
     r = np.random.default_rng(T + H + E)

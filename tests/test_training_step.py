@@ -240,7 +240,7 @@ def test_one_workspace_for_smaller_calls(moe):
     rws = torch.full((moe.moe_router_backward_workspace_bytes(T, H, E),), 0xFF, dtype=torch.uint8, device="cuda")
     wws = torch.full((moe.moe_ckpt_wgrad_workspace_bytes(T, 64, H),), 0xFF, dtype=torch.uint8, device="cuda")
     bws = torch.full((moe.moe_balance_workspace_bytes(T, E, 5),), 0xFF, dtype=torch.uint8, device="cuda")
-    for n in (T, 1, 70, 1500, 64, 65, 700):
+    for n in (T, 1, 70, 1500, 128, 129, 257, 700):
         a = moe.moe_router_logits_backward(dl[:n], w, x=x[:n], ws=rws)
         b = moe.moe_router_logits_backward(dl[:n], w, x=x[:n])
         for u, v in zip(a, b):
