@@ -56,7 +56,8 @@
 
 namespace moe {
 
-enum { GM_WGRAD = 0, GM_RDW = 1, GM_RDX = 2 };
+// (GM_WGRAD_FEW: GM_WGRAD for few rows, where storing C is what takes the time)
+enum { GM_WGRAD = 0, GM_RDW = 1, GM_RDX = 2, GM_WGRAD_FEW = 3 };
 
 constexpr int GG_TILE = 256;            // rows and columns of C per pair
 constexpr int GG_HALF = 128;            // per CTA: rows of A's tile, columns of B's
@@ -72,24 +73,35 @@ constexpr int GG_MAX_PAIRS = 128;
 constexpr int GG_REGS = 128, GG_REGS_LOAD = 64, GG_REGS_EPI = 192;
 static_assert(2 * GG_REGS_LOAD + 2 * GG_REGS_EPI <= 4 * GG_REGS, "registers of the block");
 
+// Up to 256 rows a group, GM_WGRAD_FEW: with one piece of 4 KB on its way an
+// epilogue warp waits for it, with two it stores at the copy bandwidth.  A stage
+// less pays for it, which costs where rows are many.  Measured (us, FEW / the
+// other form; N = K = 4096): 40 rows 18.0 / 21.7, 128 19.0 / 22.5, 256 20.9 / 23.2,
+// 512 27.2 / 26.3; 16 groups of 100 rows 222 / 219, of 400 326 / 268, of 800 486 / 467.
+constexpr int kFewRows = 256;
+
 template <int MODE>
 struct GradCfg {
-    static constexpr int AP = MODE == GM_WGRAD ? 1 : MODE == GM_RDW ? 3 : 2;   // parts of A
+    static constexpr bool WGRAD = MODE == GM_WGRAD || MODE == GM_WGRAD_FEW;
+    static constexpr int AP = WGRAD ? 1 : MODE == GM_RDW ? 3 : 2;   // parts of A
     static constexpr int BP = MODE == GM_RDX ? 2 : 1;
     static constexpr int OPS = (AP + BP) * GG_PLANE;
-    static constexpr int STAGES = MODE == GM_WGRAD ? 6 : 3;
-    static constexpr int ACC_STEPS = MODE == GM_WGRAD ? 16 : MODE == GM_RDW ? 4 : 16;
+    // Stages, and pieces of 4 KB that an epilogue warp has on their way out.
+    static constexpr int STAGES = MODE == GM_WGRAD ? 6 : MODE == GM_WGRAD_FEW ? 5 : 3;
+    static constexpr int OUTS = MODE == GM_WGRAD_FEW ? 2 : 1;
+    static constexpr int ACC_STEPS = WGRAD ? 16 : MODE == GM_RDW ? 4 : 16;
     // Largest chunk of a split tile, and what splitting has to save, in stages
     // (about 5 us, what k_grad_fixup adds: a stage takes 0.28 us in GM_WGRAD, 0.85 with
-    // three products; 512 tokens, 8 stages in 2: the same time with and without).  A result of GM_RDX, of at most 16 stages, is not split.
-    static constexpr int CHUNK_STEPS = MODE == GM_WGRAD ? 16 : 8;
-    static constexpr int SPLIT_GAIN = MODE == GM_WGRAD ? 18 : MODE == GM_RDW ? 8 : 1 << 20;
+    // three products; 512 tokens, 8 stages in 2: the same time with and without).  A
+    // result of GM_RDX, of at most 16 stages, is not split.
+    static constexpr int CHUNK_STEPS = WGRAD ? 16 : 8;
+    static constexpr int SPLIT_GAIN = WGRAD ? 18 : MODE == GM_RDW ? 8 : 1 << 20;
 };
 
 template <int MODE>
 struct GradShared {
     uint8_t ops[GradCfg<MODE>::STAGES][GradCfg<MODE>::OPS];      // 1024-byte aligned
-    uint8_t out[GG_EPI_WARPS][GG_OUT];               // epilogue: 32 rows of 128 bytes per warp
+    uint8_t out[GG_EPI_WARPS][GradCfg<MODE>::OUTS][GG_OUT];   // epilogue: 32 rows of 128 bytes each
     uint64_t landed[GradCfg<MODE>::STAGES];          // leader: TMA bytes of both CTAs
     uint64_t tail_landed[GradCfg<MODE>::STAGES];     // a stage with a tail: those of this CTA
     uint64_t tail[GradCfg<MODE>::STAGES];            // its rows behind the group are cleared
@@ -492,7 +504,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     // of each stage's barriers of either kind.
     uint32_t lands = 0, tails = 0;
     auto has_tail = [&](const Segment& s, int st) {
-        return MODE == GM_WGRAD && s.r1 < a.R && s.r1 - s.r0 - st * GG_K < GG_K;
+        return Cfg::WGRAD && s.r1 < a.R && s.r1 - s.r0 - st * GG_K < GG_K;
     };
     auto next_parity = [&](uint32_t& bits) {
         const uint32_t p = bits >> stage & 1u;
@@ -515,7 +527,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                     give_up();
                     break;
                 }
-                if (MODE == GM_WGRAD && a.withhold && first) {
+                if (Cfg::WGRAD && a.withhold && first) {
                     first = false;
                     next_stage();
                     continue;
@@ -596,7 +608,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                                            !(first && s == st && kk == 0));
                                 }
                             };
-                            if constexpr (MODE == GM_WGRAD) {
+                            if constexpr (Cfg::WGRAD) {
                                 product(0, 0, true);
                             } else if constexpr (MODE == GM_RDW) {
                                 product(2, 0, true);
@@ -621,7 +633,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             }
             // every MMA is done before either CTA frees its TMEM
             final_wait(smem_u32(&sh.drain), 0);
-        } else if (MODE == GM_WGRAD && warp == 2 && a.perm) {
+        } else if (Cfg::WGRAD && warp == 2 && a.perm) {
             // (k_grad_prepare reads row 0 for a bad entry; the error word is this
             // call's only from the second kernel on)
             int r0 = 0, r1 = a.R, unused;
@@ -637,13 +649,13 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         __syncwarp();
     } else if (warp < GG_EPI_WARP0) {
         gg_regs_down<GG_REGS_LOAD>();
-        if (MODE != GM_WGRAD && a.bias.part) {
+        if (!Cfg::WGRAD && a.bias.part) {
             for (int b = blockIdx.x; b * 32 < a.bias.E; b += gridDim.x) {
                 grad_bias(a.bias, b, threadIdx.x - 32 * GG_TAIL_WARP0, sh.bias);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
         }
-        if (MODE == GM_WGRAD && a.offsets) {
+        if (Cfg::WGRAD && a.offsets) {
             // ---------------- rows behind a group's last one ----------------
             const int t = threadIdx.x - 32 * GG_TAIL_WARP0;
             for (Steps s(walk0); s.on; s.advance()) {
@@ -678,7 +690,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         // bank conflicts) and TMA, which writes whole lines and cuts off what
         // lies outside C; adding to C is its reduction.
         const int q = warp & 3, half = (warp - GG_EPI_WARP0) >> 2;
-        const uint32_t out = smem_u32(sh.out[warp - GG_EPI_WARP0]);
+        int piece = 0;
         int buf = 0;
         uint32_t use = 0;
         Walk walk(walk0);
@@ -716,9 +728,11 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
 #pragma unroll
             for (int g = 0; g < 128 / COLS; ++g) {
                 if (nc + COLS * g < seg.c0 || nc + COLS * g >= seg.c1) continue;
-                // the previous 32 x 128 bytes have been read
-                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                // what was in this piece has been read
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(Cfg::OUTS - 1) : "memory");
                 __syncwarp();
+                const uint32_t out = smem_u32(sh.out[warp - GG_EPI_WARP0][piece]);
+                piece = piece + 1 == Cfg::OUTS ? 0 : piece + 1;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     uint4 v;
@@ -1201,7 +1215,9 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
     a.flag = flag;
     a.wait_ns = wait_ns;
     a.withhold = withhold;
-    return launch_grad<GM_WGRAD>(a, a_map, b_map, dw, st);
+    // (rows of a group: the average stands for them)
+    return R / G <= kFewRows ? launch_grad<GM_WGRAD_FEW>(a, a_map, b_map, dw, st)
+                             : launch_grad<GM_WGRAD>(a, a_map, b_map, dw, st);
 }
 
 cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t* codes, const uint8_t* scales,
