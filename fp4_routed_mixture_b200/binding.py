@@ -430,10 +430,12 @@ def _arg(t, name: str, dtype, shape, dev, strided: bool = False):
     return t.data_ptr()
 
 
-def _row_stride(t) -> int:
-    """Elements between the rows of a checked 2-D tensor (a single row's stride
-    means nothing and counts as its length)."""
-    return t.stride(0) if t.shape[0] > 1 and not t.is_contiguous() else t.shape[1]
+def _rows(t, name: str, dtype, shape, dev):
+    """(pointer, elements from row to row) of a checked 2-D tensor whose rows may
+    lie further apart than their length (a single row's stride means nothing and
+    counts as its length)."""
+    p = _arg(t, name, dtype, shape, dev, True)
+    return p, shape[1] if shape[0] < 2 or t.is_contiguous() else t.stride(0)
 
 
 def _matrix(t, name: str):
@@ -484,7 +486,7 @@ def _call(dev, fn, args, stream):
         if stream.device != dev:
             _bad(f"stream is on {stream.device}, the tensors on {dev}")
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -591,9 +593,9 @@ def moe_ckpt_pack(x, out=None, stream=None):
         out = (_new((T, K), torch.uint8, dev, stream),
                _new((T, K // 128), torch.uint8, dev, stream))
     codes, scales = out
-    px = _arg(x, "x", torch.bfloat16, (T, K), dev, strided=True)
+    px, ldx = _rows(x, "x", torch.bfloat16, (T, K), dev)
     o = (_arg(codes, "codes", torch.uint8, (T, K), dev), _arg(scales, "scales", torch.uint8, (T, K // 128), dev))
-    _call(dev, lib.moe_ckpt_pack, (px, _row_stride(x), T, K, *o), stream)
+    _call(dev, lib.moe_ckpt_pack, (px, ldx, T, K, *o), stream)
     return out
 
 
@@ -604,8 +606,7 @@ def moe_ckpt_unpack(codes, scales, out=None, stream=None):
     if out is None:
         out = _new((T, K), torch.bfloat16, dev, stream)
     p = (_arg(codes, "codes", torch.uint8, (T, K), dev), _arg(scales, "scales", torch.uint8, (T, K // 128), dev))
-    po = _arg(out, "out", torch.bfloat16, (T, K), dev, strided=True)
-    _call(dev, lib.moe_ckpt_unpack, (*p, T, K, po, _row_stride(out)), stream)
+    _call(dev, lib.moe_ckpt_unpack, (*p, T, K, *_rows(out, "out", torch.bfloat16, (T, K), dev)), stream)
     return out
 
 
@@ -622,7 +623,7 @@ def moe_ckpt_swiglu_backward(gu_codes, gu_scales, dh, need_h: bool = False, out=
         _bad("out holds no tensor for h")
     p = (_arg(gu_codes, "gu_codes", torch.uint8, (T, 2 * I), dev),
          _arg(gu_scales, "gu_scales", torch.uint8, (T, 2 * I // 128), dev),
-         _arg(dh, "dh", torch.bfloat16, (T, I), dev, strided=True), _row_stride(dh), T, I,
+         *_rows(dh, "dh", torch.bfloat16, (T, I), dev), T, I,
          _arg(dgu, "dgu", torch.bfloat16, (T, 2 * I), dev),
          _arg(h, "h", torch.bfloat16, (T, I), dev) if need_h else None)
     _call(dev, lib.moe_ckpt_swiglu_backward, p, stream)
@@ -650,7 +651,7 @@ def moe_ckpt_wgrad(dy, codes, scales, offsets=None, perm=None, k: int = 1, dw=No
         if accumulate:
             _bad("accumulate needs dw")
         dw = _new(shape, torch.float32, dev, stream)
-    p = (_arg(dy, "dy", torch.bfloat16, (R, N), dev, strided=True), _row_stride(dy),
+    p = (*_rows(dy, "dy", torch.bfloat16, (R, N), dev),
          _arg(codes, "codes", torch.uint8, (X, K), dev), _arg(scales, "scales", torch.uint8, (X, K // 128), dev),
          _arg(offsets, "offsets", torch.int32, (G + 1,), dev), _arg(perm, "perm", torch.int32, (R,), dev))
     pd = _arg(dw, "dw", torch.float32, shape, dev)
