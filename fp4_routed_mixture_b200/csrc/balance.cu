@@ -15,7 +15,7 @@
 // for any ragged split.  No two additions to one address race: results do not
 // depend on the order in which CTAs run.
 // All three read [T, E] once (the backward also writes it): HBM bound when T is
-// large.  One B200, 65536 x 256 logits in 16 sequences: loss 21 us (3.2 TB/s; a
+// large.  One B200, 65536 x 256 logits in 16 sequences: loss 20 us (3.4 TB/s; a
 // warp's row is short, and two rows per warp, other block sizes and more blocks
 // measured 17 to 25 us for the rows but no less in all), gradient 28 us.
 #include "kernels.cuh"
@@ -26,7 +26,7 @@ namespace moe {
 constexpr int kBalThreads = 512;             // k_balance_rows: 2 CTAs per SM
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalMaxChunks = 148 * 2;
-constexpr int kRedThreads = 256, kRedWarps = kRedThreads / 32;
+constexpr int kRedThreads = 1024, kRedWarps = kRedThreads / 32;
 // Calls of at most this many rows and sequences run in one CTA and launch (8
 // rows of 256 logits: one launch of 3 us less).
 constexpr int kBalSingleT = 128, kBalSingleS = 64;
@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_rows(BalanceArgs a) {
     }
 }
 
-// CTA (column block of 32, sequence): 8 warps take every eighth chunk of the
-// sequence, lane = column; the eight sums are added in warp order.
+// CTA (column block of 32, sequence): 32 warps take every 32nd chunk of the
+// sequence, lane = column; the warps' sums are added in warp order.
 __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(BalanceArgs a) {
     pdl_begin();
     __shared__ float sp[kRedWarps][33];
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(BalanceArgs a) {
         n = 0;
         p = 0.0f;
         h = 0;
-#pragma unroll
+#pragma unroll 8
         for (int w = 0; w < kRedWarps; ++w) {
             n += sn[w];
             p += sp[w][lane];
