@@ -539,8 +539,8 @@ def moe_route_backward(logits, topk_idx, gates=None, dgates=None, dloss=None, co
     S = 1 if seq_offsets is None else _table(seq_offsets, "seq_offsets")
     if out is None:
         out = _new((T, E), torch.float32, dev, stream)
-    if ws is not None and ws.numel() < 4:
-        _bad("ws must hold at least 4 bytes")
+    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.numel() < 4):
+        _bad("ws must be a tensor of at least 4 bytes")
     p = (_arg(logits, "logits", torch.float32, (T, E), dev), _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
          _arg(gates, "gates", torch.float32, (T, k), dev), _arg(dgates, "dgates", torch.float32, (T, k), dev),
          _arg(dloss, "dloss", torch.float32, (1,), dev), _arg(counts, "counts", torch.int32, (S, E), dev),

@@ -641,8 +641,23 @@ int moe_fp8_linear(const void* x_bf16, int T, int N, int K, const void* packed, 
 
 // ---- Training: balance loss, gradients, 8-bit checkpoints ----------------------
 
+// Rows and columns whose products and sums the kernels hold in 32 bits.
+constexpr int kTrainMaxRows = 1 << 30, kTrainMaxCols = 1 << 20;
+
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    return a && b && na && nb && (const char*)a < (const char*)b + nb && (const char*)b < (const char*)a + na;
+}
+// Bytes from the first to the last of T rows of `cols` bf16, ld apart.
+static size_t span_bf16(int T, int cols, int64_t ld) { return T > 0 ? 2 * ((size_t)(T - 1) * ld + cols) : 0; }
+
+static int check_train_rows(int T, const char* who) {
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative number of rows", who);
+    if (T > kTrainMaxRows) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: at most 2^30 rows (got %d)", who, T);
+    return MOE_OK;
+}
+
 static int check_balance_dims(int T, int E, int k, int S, bool has_seq, const char* who) {
-    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T < 0", who);
+    if (int rc = check_train_rows(T, who)) return rc;
     if (E < 1 || E > 1024) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: E must be in [1, 1024] (got %d)", who, E);
     if (k < 1 || k > 16 || k > E)
         return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: k must be in [1, min(E, 16)] (got %d)", who, k);
@@ -652,7 +667,7 @@ static int check_balance_dims(int T, int E, int k, int S, bool has_seq, const ch
 }
 
 size_t moe_balance_workspace_bytes(int T_max, int E, int S_max) {
-    if (T_max < 0 || E < 1 || E > 1024 || S_max < 1 || S_max > 65535) return 0;
+    if (T_max < 0 || T_max > kTrainMaxRows || E < 1 || E > 1024 || S_max < 1 || S_max > 65535) return 0;
     return moe::balance_workspace_bytes(T_max, E, S_max);
 }
 
@@ -689,7 +704,7 @@ int moe_route_backward(const float* logits, const int32_t* topk_idx, const float
         !aligned(dlogits, 4) || !aligned(flag, 4))
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: the tensors need 4-byte alignment");
     const size_t bytes = 4 * (size_t)T * E;
-    if (T > 0 && (const char*)logits < (const char*)dlogits + bytes && (const char*)dlogits < (const char*)logits + bytes)
+    if (overlap(dlogits, bytes, logits, bytes))
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: dlogits overlaps logits");
     cudaError_t e = moe::launch_route_backward(logits, topk_idx, gates, dgates, dloss, counts, tokens, seq_offsets,
                                                token_mask, T, E, k, S, coef, dlogits, flag, stream);
@@ -697,7 +712,7 @@ int moe_route_backward(const float* logits, const int32_t* topk_idx, const float
 }
 
 size_t moe_router_backward_workspace_bytes(int T_max, int H, int E) {
-    if (T_max < 0 || H <= 0 || H % 32 || E < 1 || E > 1024) return 0;
+    if (T_max < 0 || T_max > kTrainMaxRows || H <= 0 || H % 32 || H > kTrainMaxCols || E < 1 || E > 1024) return 0;
     return moe::router_backward_workspace_bytes(T_max, H, E);
 }
 
@@ -707,8 +722,9 @@ int moe_router_logits_backward(const float* dlogits, const void* x_bf16, const u
                                cudaStream_t stream) {
     g_last_error.clear();
     const char* who = "moe_router_logits_backward";
-    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T < 0", who);
-    if (H <= 0 || H % 32) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H must be a positive multiple of 32 (got %d)", who, H);
+    if (int rc = check_train_rows(T, who)) return rc;
+    if (H <= 0 || H % 32 || H > kTrainMaxCols)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H must be a multiple of 32 in [32, 2^20] (got %d)", who, H);
     if (E < 1 || E > 1024) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: E must be in [1, 1024] (got %d)", who, E);
     if (accumulate != 0 && accumulate != 1) return fail(MOE_ERR_INVALID_ARG, "%s: accumulate must be 0 or 1", who);
     if (!dx_bf16 && !dw && !dbias) return fail(MOE_ERR_INVALID_ARG, "%s: dx, dw and dbias are all NULL", who);
@@ -726,13 +742,20 @@ int moe_router_logits_backward(const float* dlogits, const void* x_bf16, const u
     if (ws_bytes < moe::router_backward_workspace_bytes(T, H, E))
         return fail(MOE_ERR_INVALID_ARG, "%s: ws_bytes %zu < %zu", who, ws_bytes,
                     moe::router_backward_workspace_bytes(T, H, E));
+    const size_t dl_n = 4 * (size_t)T * E, w_n = 4 * (size_t)E * H, x_n = (size_t)T * H;
+    if (overlap(dx_bf16, 2 * x_n, dlogits, dl_n) || overlap(dx_bf16, 2 * x_n, x_bf16, 2 * x_n) ||
+        overlap(dx_bf16, 2 * x_n, x_codes, x_n) || overlap(dx_bf16, 2 * x_n, w_router, w_n) ||
+        overlap(dw, w_n, dlogits, dl_n) || overlap(dw, w_n, x_bf16, 2 * x_n) || overlap(dw, w_n, x_codes, x_n) ||
+        overlap(dw, w_n, w_router, w_n) || overlap(dx_bf16, 2 * x_n, dw, w_n) ||
+        overlap(dbias, 4 * (size_t)E, dlogits, dl_n))
+        return fail(MOE_ERR_INVALID_ARG, "%s: an output overlaps an input or the other output", who);
     cudaError_t e = moe::launch_router_backward(dlogits, x_bf16, x_codes, x_scales, w_router, T, H, E, dx_bf16, dw,
                                                 dbias, accumulate, ws, load_options().wait_ns, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, who);
 }
 
 static int check_ckpt_dims(int T, int K, const char* who) {
-    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative number of rows", who);
+    if (int rc = check_train_rows(T, who)) return rc;
     if (K <= 0 || K % 128 || K > (1 << 24))
         return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: the row length must be a positive multiple of 128 (got %d)", who, K);
     return MOE_OK;
@@ -752,6 +775,9 @@ int moe_ckpt_pack(const void* x_bf16, int64_t ldx, int T, int K, uint8_t* codes,
     if (T > 0 && (!x_bf16 || !codes || !scales)) return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_pack: NULL pointer");
     if (!aligned(x_bf16, 16) || !aligned(codes, 16))
         return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_pack: x and codes need 16-byte alignment");
+    const size_t n = (size_t)T * K, xn = span_bf16(T, K, ldx);
+    if (overlap(codes, n, x_bf16, xn) || overlap(scales, n / 128, x_bf16, xn))
+        return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_pack: the checkpoint overlaps x");
     cudaError_t e = moe::launch_ckpt_pack(x_bf16, ldx, T, K, codes, scales, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_ckpt_pack launch");
 }
@@ -764,6 +790,9 @@ int moe_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int T, int K, v
     if (T > 0 && (!x_bf16 || !codes || !scales)) return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_unpack: NULL pointer");
     if (!aligned(x_bf16, 16) || !aligned(codes, 16))
         return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_unpack: x and codes need 16-byte alignment");
+    const size_t n = (size_t)T * K, xn = span_bf16(T, K, ldx);
+    if (overlap(codes, n, x_bf16, xn) || overlap(scales, n / 128, x_bf16, xn))
+        return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_unpack: x overlaps the checkpoint");
     cudaError_t e = moe::launch_ckpt_unpack(codes, scales, T, K, x_bf16, ldx, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_ckpt_unpack launch");
 }
@@ -778,13 +807,19 @@ int moe_ckpt_swiglu_backward(const uint8_t* gu_codes, const uint8_t* gu_scales, 
         return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
     if (!aligned(gu_codes, 16) || !aligned(dh_bf16, 16) || !aligned(dgu_bf16, 16) || !aligned(h_bf16, 16))
         return fail(MOE_ERR_INVALID_ARG, "%s: codes, dh, dgu and h need 16-byte alignment", who);
+    const size_t n = (size_t)T * I, dn = span_bf16(T, I, lddh);
+    if (overlap(dgu_bf16, 4 * n, gu_codes, 2 * n) || overlap(dgu_bf16, 4 * n, gu_scales, 2 * n / 128) ||
+        overlap(dgu_bf16, 4 * n, dh_bf16, dn) || overlap(dgu_bf16, 4 * n, h_bf16, 2 * n) ||
+        overlap(h_bf16, 2 * n, gu_codes, 2 * n) || overlap(h_bf16, 2 * n, gu_scales, 2 * n / 128) ||
+        overlap(h_bf16, 2 * n, dh_bf16, dn))
+        return fail(MOE_ERR_INVALID_ARG, "%s: an output overlaps an input or the other output", who);
     cudaError_t e = moe::launch_ckpt_swiglu_backward(gu_codes, gu_scales, dh_bf16, lddh, T, I, dgu_bf16, h_bf16, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, who);
 }
 
 static bool wgrad_dims_ok(int R, int N, int K, int G) {
-    return R >= 0 && N > 0 && N % 8 == 0 && N <= (1 << 20) && K > 0 && K % 128 == 0 && K <= (1 << 20) && G >= 1 &&
-           G <= 1024;
+    return R >= 0 && R <= kTrainMaxRows && N > 0 && N % 8 == 0 && N <= kTrainMaxCols && K > 0 && K % 128 == 0 &&
+           K <= kTrainMaxCols && G >= 1 && G <= 1024;
 }
 
 size_t moe_ckpt_wgrad_workspace_bytes(int R_max, int N, int K, int G) {
@@ -797,7 +832,8 @@ int moe_ckpt_wgrad(const void* dy_bf16, int64_t lddy, const uint8_t* x_codes, co
                    float* dw, int accumulate, void* ws, size_t ws_bytes, cudaStream_t stream) {
     g_last_error.clear();
     const char* who = "moe_ckpt_wgrad";
-    if (R < 0 || X < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative number of rows", who);
+    if (int rc = check_train_rows(R, who)) return rc;
+    if (int rc = check_train_rows(X, who)) return rc;
     if (!wgrad_dims_ok(R, N, K, G))
         return fail(MOE_ERR_UNSUPPORTED_SHAPE,
                     "%s: N must be a multiple of 8, K of 128 (both at most 2^20), G in [1, 1024] (N=%d K=%d G=%d)",
@@ -816,6 +852,9 @@ int moe_ckpt_wgrad(const void* dy_bf16, int64_t lddy, const uint8_t* x_codes, co
     if (ws_bytes < moe::wgrad_workspace_bytes(R, N, K, G))
         return fail(MOE_ERR_INVALID_ARG, "%s: ws_bytes %zu < %zu", who, ws_bytes,
                     moe::wgrad_workspace_bytes(R, N, K, G));
+    const size_t wn = 4 * (size_t)G * N * K;
+    if (overlap(dw, wn, dy_bf16, span_bf16(R, N, lddy)) || overlap(dw, wn, x_codes, (size_t)X * K))
+        return fail(MOE_ERR_INVALID_ARG, "%s: dw overlaps an input", who);
     cudaError_t e = moe::launch_ckpt_wgrad(dy_bf16, lddy, x_codes, x_scales, offsets, perm, k_div, R, X, N, K, G, dw,
                                            accumulate, ws, load_options().wait_ns,
                                            R > 0 ? g_test_grad_timeout.exchange(0) : 0, stream);

@@ -315,7 +315,8 @@ int moe_fp8_linear(const void *x_bf16, int T, int N, int K, const void *packed, 
  * no training; these calls use the usual definitions and this library's own
  * routing (moe_route), sort (moe_sort) and FP8 block format (moe_fp8_linear).
  * All are asynchronous and graph-capturable, and their results do not depend
- * on the order in which thread blocks run.  A workspace (and its error word)
+ * on the order in which thread blocks run.  They take at most 2^30 rows, and no
+ * output may overlap an input or another output.  A workspace (and its error word)
  * belongs to one call at a time: calls and replayed graphs that may overlap
  * need one each.
  * ------------------------------------------------------------------------- */
@@ -377,10 +378,12 @@ int moe_route_backward(const float *logits, const int32_t *topk_idx, const float
  * Small calls (up to 128 tokens, or 256) use fp32 multiply-adds.  Larger ones form the
  * products of fp32 operands from bf16 parts on the tensor cores, accumulated in
  * fp32: dw from all three parts of dlogits (exact), dx from the leading two
- * parts of each operand (about 16 bits, before its rounding to 8).
+ * parts of each operand (about 16 bits, before its rounding to 8).  An infinity
+ * in dlogits, x or w_router makes the sums it enters infinite or NaN (in parts,
+ * infinity times a part of 0 is NaN).
  * ws: moe_router_backward_workspace_bytes(T_max, H, E) bytes, 256-byte
  * aligned, T <= T_max; first int32: the error word, cleared by this call
- * (MOE_FLAG_TIMEOUT as in moe_forward).  H % 32 == 0, 1 <= E <= 1024; dlogits,
+ * (MOE_FLAG_TIMEOUT as in moe_forward).  H % 32 == 0, H <= 2^20, 1 <= E <= 1024; dlogits,
  * x_bf16, x_codes, w_router, dx, dw 16-byte aligned.  T == 0 leaves dw and
  * dbias 0 (accumulate 1: unchanged). */
 size_t moe_router_backward_workspace_bytes(int T_max, int H, int E);

@@ -88,6 +88,43 @@ def test_refused(fn, args, status):
     assert moe.moe_launch_count() == before
 
 
+M = (1 << 30) + 1                 # more rows than a call takes
+F = [(k + 2) << 36 for k in range(10)]      # pointers 64 GB apart
+
+
+@pytest.mark.parametrize("fn,args,status", [
+    (balance, dict(T=M), SHAPE), (route, dict(T=M), SHAPE), (router, dict(T=M), SHAPE), (pack, dict(T=M), SHAPE),
+    (unpack, dict(T=M), SHAPE), (swiglu, dict(T=M), SHAPE), (wgrad, dict(R=M, X=M), SHAPE),
+    (wgrad, dict(R=4, X=M), SHAPE), (balance, dict(T=(1 << 31) - 1), SHAPE), (router, dict(H=(1 << 20) + 32), SHAPE),
+])
+def test_too_large(fn, args, status):
+    assert fn(**args) == status
+
+
+ROUTER = dict(dl=F[0], x=F[1], w=F[2], dx=F[3], dw=F[4], db=F[5], ws=F[6], T=4, H=128, E=16)
+SWIGLU = dict(codes=F[0], scales=F[1], dh=F[2], dgu=F[3], h=F[4])
+WGRAD = dict(dy=F[0], codes=F[1], scales=F[2], dw=F[3], ws=F[4])
+
+
+@pytest.mark.parametrize("fn,args", [
+    (router, {**ROUTER, "dx": F[1]}), (router, {**ROUTER, "dx": F[1] + 4 * 128 * 2 - 16}),
+    (router, {**ROUTER, "dx": F[0]}), (router, {**ROUTER, "dx": F[2]}), (router, {**ROUTER, "dw": F[2]}),
+    (router, {**ROUTER, "dw": F[0]}), (router, {**ROUTER, "dw": F[3]}), (router, {**ROUTER, "db": F[0] + 16}),
+    (router, {**ROUTER, "x": None, "codes": F[1], "scales": F[7], "dx": F[1]}),
+    (pack, dict(x=F[0], codes=F[0], scales=F[1])), (pack, dict(x=F[0], codes=F[1], scales=F[0] + 4 * 256 - 1)),
+    (unpack, dict(x=F[0], codes=F[0] + 512, scales=F[1])),
+    (unpack, dict(x=F[0], ld=256, codes=F[0] + 1536, scales=F[1])),
+    (swiglu, {**SWIGLU, "dgu": F[0]}), (swiglu, {**SWIGLU, "dgu": F[2]}), (swiglu, {**SWIGLU, "h": F[2]}),
+    (swiglu, {**SWIGLU, "h": F[3] + 16}), (swiglu, {**SWIGLU, "h": F[0]}),
+    (wgrad, {**WGRAD, "dw": F[0]}), (wgrad, {**WGRAD, "dw": F[1] + 496}),
+])
+def test_overlapping_outputs_refused(fn, args):
+    before = moe.moe_launch_count()
+    assert fn(**args) == INVALID
+    assert "overlap" in moe.binding.last_error()
+    assert moe.moe_launch_count() == before
+
+
 def test_size_queries():
     assert moe.moe_balance_workspace_bytes(0, 1, 1) > 0
     # a workspace for T_max serves every smaller call
@@ -101,7 +138,11 @@ def test_size_queries():
     for bad in (lambda: moe.moe_balance_workspace_bytes(4, 1025, 1), lambda: moe.moe_balance_workspace_bytes(4, 8, 0),
                 lambda: moe.moe_router_backward_workspace_bytes(4, 100, 8),
                 lambda: moe.moe_ckpt_wgrad_workspace_bytes(4, 60, 128, 1),
-                lambda: moe.moe_ckpt_wgrad_workspace_bytes(4, 64, 64, 1)):
+                lambda: moe.moe_ckpt_wgrad_workspace_bytes(4, 64, 64, 1),
+                lambda: moe.moe_balance_workspace_bytes(M, 8, 1),
+                lambda: moe.moe_router_backward_workspace_bytes(M, 64, 8),
+                lambda: moe.moe_router_backward_workspace_bytes(4, (1 << 20) + 32, 8),
+                lambda: moe.moe_ckpt_wgrad_workspace_bytes(M, 64, 128, 1)):
         with pytest.raises(moe.MoeError) as e:
             bad()
         assert e.value.status == SHAPE
