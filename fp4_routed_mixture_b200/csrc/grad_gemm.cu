@@ -112,6 +112,7 @@ struct GradShared {
     int32_t abort;
     int32_t rem_pre[GG_MAX_PAIRS + 1];               // chunks in front of each split tile
     float bias[4][32];
+    uint8_t slots[MODE == GM_RDX ? 4 : 1][GG_MAX_PAIRS];
 };
 
 // dbias: column sums over the row blocks that k_grad_prepare summed.  128 threads
@@ -154,10 +155,18 @@ struct GradArgs {
     float* c;                  // (GM_RDX stores through its map alone)
     int accumulate;
     float* part;               // [pairs][2][256][256]
+    const uint8_t* x_scales;   // GM_RDW: B is a checkpoint's codes with these scales, or NULL
     BiasArgs bias;             // GM_RDW, GM_RDX
     int32_t* flag;
     uint64_t wait_ns;
     int withhold;              // a test: no pair's first stage is copied
+};
+
+// Split tiles of a launch in front whose parts are still to be added (a.part NULL:
+// none); pairs: of that launch.
+struct FixupArgs {
+    GradArgs a;
+    int pairs;
 };
 
 // ---- PTX forms of the SM pair ----------------------------------------------------
@@ -396,10 +405,89 @@ struct Steps {
     }
 };
 
+// ---- the parts of split tiles ------------------------------------------------------------
+// Adds them in the order of their rows.  A warp takes rows [lo, hi) of the split
+// tiles' rows, tile after tile; slots: GG_MAX_PAIRS bytes of its own.
+__device__ __forceinline__ void grad_fixup(const GradArgs& a, int pairs, int lo, int hi, uint8_t* slots) {
+    const int rem = a.tiles - a.full, per = a.MT * a.NT, lane = threadIdx.x & 31;
+    int tile = -1, n = 0;
+    for (int row = lo; row < hi; ++row) {
+        const int i = row / GG_TILE, m = row % GG_TILE, t = a.full + i;
+        if (i != tile) {
+            // chunks of all split tiles, of those in front of tile i, and its own
+            tile = i;
+            int all = 0, b = 0, own = 0;
+            for (int j = lane; j < rem; j += 32) {
+                int r0, r1;
+                gg_rows(a, (a.full + j) / per, r0, r1);
+                const int c = (gg_steps(r1 - r0) + a.chunk_steps - 1) / a.chunk_steps;
+                all += c;
+                b += j < i ? c : 0;
+                own += j == i ? c : 0;
+            }
+            const long long W = warp_sum(all);
+            b = warp_sum(b);
+            const int e = b + warp_sum(own);
+            // the pairs whose range of chunks meets the tile's, in order
+            n = 0;
+            __syncwarp();
+            for (int p0 = 0; p0 < pairs; p0 += 32) {
+                const int p = p0 + lane, c0 = (int)(W * p / pairs), c1 = (int)(W * (p + 1) / pairs);
+                const bool in = p < pairs && c0 < c1 && c0 < e && c1 > b;
+                const uint32_t mask = __ballot_sync(0xffffffffu, in);
+                // (it is a pair's second part where the pair's range begins in an earlier tile)
+                if (in) slots[n + __popc(mask & ((1u << lane) - 1))] = (uint8_t)(2 * p + (c0 < b ? 1 : 0));
+                n += __popc(mask);
+            }
+            __syncwarp();
+        }
+        if (n == 1) continue;        // one pair computed the whole tile
+        int m0, n0;
+        gg_tile(a, t % per, m0, n0);
+        if (m0 + m >= a.M) continue;
+        float* out = a.c + ((size_t)(t / per) * a.M + m0 + m) * a.N + n0;
+        const float* part = a.part + m * GG_TILE;
+        float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const float4* p = reinterpret_cast<const float4*>(part + (size_t)slots[j] * (GG_TILE * GG_TILE)) + lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 v = __ldg(p + 32 * h);
+                s[h].x = __fadd_rn(s[h].x, v.x);
+                s[h].y = __fadd_rn(s[h].y, v.y);
+                s[h].z = __fadd_rn(s[h].z, v.z);
+                s[h].w = __fadd_rn(s[h].w, v.w);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = 4 * lane + 128 * h;
+            if (n0 + c >= a.N) continue;
+            float4* o = reinterpret_cast<float4*>(out + c);
+            if (a.accumulate) {
+                const float4 v = *o;
+                s[h].x = __fadd_rn(v.x, s[h].x);
+                s[h].y = __fadd_rn(v.y, s[h].y);
+                s[h].z = __fadd_rn(v.z, s[h].z);
+                s[h].w = __fadd_rn(v.w, s[h].w);
+            }
+            *o = s[h];
+        }
+    }
+}
+// CTA: 8 rows, a warp each.
+__global__ void __launch_bounds__(256) k_grad_fixup(FixupArgs f) {
+    pdl_begin();
+    __shared__ uint8_t slots[8][GG_MAX_PAIRS];
+    const int warp = threadIdx.x >> 5, row = blockIdx.x * 8 + warp;
+    grad_fixup(f.a, f.pairs, row, row + 1, slots[warp]);
+}
+
 // ---- the kernel ----------------------------------------------------------------------
 template <int MODE>
 __global__ void __launch_bounds__(GG_THREADS, 1)
-    k_grad_gemm(const __grid_constant__ GradArgs a, const __grid_constant__ CUtensorMap a_map,
+    k_grad_gemm(const __grid_constant__ GradArgs a, const __grid_constant__ FixupArgs fix, const __grid_constant__ CUtensorMap a_map,
                 const __grid_constant__ CUtensorMap b_map, const __grid_constant__ CUtensorMap c_map,
                 const __grid_constant__ CUtensorMap part_map) {
     using Cfg = GradCfg<MODE>;
@@ -506,6 +594,8 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     auto has_tail = [&](const Segment& s, int st) {
         return Cfg::WGRAD && s.r1 < a.R && s.r1 - s.r0 - st * GG_K < GG_K;
     };
+    // B comes as a checkpoint's codes, which warps 4-7 turn into bf16.
+    const bool convert = MODE == GM_RDW && a.x_scales;
     auto next_parity = [&](uint32_t& bits) {
         const uint32_t p = bits >> stage & 1u;
         bits ^= 1u << stage;
@@ -520,7 +610,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             // waits here run to their limit even when another role has given
             // up: "empty" reaches both CTAs, so both have then issued the same
             // stages, and the leader's last waits cover the copies of both.)
-            constexpr uint32_t bytes = (AP + BP) * GG_PLANE;
+            const uint32_t bytes = (convert ? AP : AP + BP) * GG_PLANE;
             bool first = true;
             for (Steps s(walk0); s.on; s.advance()) {
                 if (!gg_wait(smem_u32(&sh.empty[stage]), phase ^ 1u, drain_ns, nullptr)) {
@@ -552,10 +642,18 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                         gg_tma(dst + GG_BLOCK, &a_map, m + 64, r, p, bar);
                     }
                 }
+                if (convert) {
+                    // 128 codes of each row, where their values will be
+                    bar = smem_u32(&sh.tail_landed[stage]);
+                    mbar_expect_tx(bar, GG_K * GG_HALF);
+                    next_parity(tails);
+                    gg_tma(dst, &b_map, n, r, 0, bar);
+                } else {
 #pragma unroll
-                for (int p = 0; p < BP; ++p, dst += GG_PLANE) {
-                    gg_tma(dst, &b_map, n, r, p, bar);
-                    gg_tma(dst + GG_BLOCK, &b_map, n + 64, r, p, bar);
+                    for (int p = 0; p < BP; ++p, dst += GG_PLANE) {
+                        gg_tma(dst, &b_map, n, r, p, bar);
+                        gg_tma(dst + GG_BLOCK, &b_map, n + 64, r, p, bar);
+                    }
                 }
                 next_stage();
             }
@@ -590,7 +688,9 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                                 const uint32_t p = next_parity(tails);
                                 in = wait(smem_u32(&sh.tail[stage]), p) && wait(smem_u32(&sh.peer[stage]), p);
                             } else {
-                                in = wait(smem_u32(&sh.landed[stage]), next_parity(lands));
+                                const uint32_t p = next_parity(lands);
+                                in = wait(smem_u32(&sh.landed[stage]), p) &&
+                                     (!convert || (wait(smem_u32(&sh.tail[stage]), p) && wait(smem_u32(&sh.peer[stage]), p)));
                             }
                             if (!in) {
                                 give_up();
@@ -649,6 +749,81 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         __syncwarp();
     } else if (warp < GG_EPI_WARP0) {
         gg_regs_down<GG_REGS_LOAD>();
+        if (convert) {
+            // ---------------- codes to bf16 ----------------
+            // 64 rows of 128 codes, 16 at a time: thread t takes columns 16 (t % 8)
+            // .. of rows t / 8 + 16 u.  The values go where the codes were.
+            const int t = threadIdx.x - 32 * GG_TAIL_WARP0, c16 = t & 7, row = t >> 3;
+            Steps s(walk0);
+            uint32_t scale[4];
+            auto fetch = [&]() {       // scale bytes, one stage ahead
+                const int n = s.seg.n0 + GG_HALF * (int)rank, r = s.seg.r0 + s.st * GG_K + row;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    scale[u] = n < a.N && r + 16 * u < a.R
+                                   ? __ldg(a.x_scales + (((size_t)(r + 16 * u) * a.N + n) >> 7)) : 0u;
+            };
+            if (s.on) fetch();
+            while (s.on) {
+                const bool in = warp_wait(smem_u32(&sh.tail_landed[stage]), next_parity(tails));
+                const uint32_t dst = smem_u32(sh.ops[stage]) + AP * GG_PLANE;
+                uint4 q[4];
+                float f[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(q[u].x), "=r"(q[u].y), "=r"(q[u].z), "=r"(q[u].w)
+                                 : "r"(dst + 16 * (t + 128 * u)));
+                    f[u] = ckpt_scale(scale[u]);
+                }
+                // all codes are read; the four warps go on or give up together
+                uint32_t all;
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\t"
+                    "setp.ne.u32 p, %1, 0;\n\t"
+                    "bar.red.and.pred q, 1, 128, p;\n\t"
+                    "selp.u32 %0, 1, 0, q;\n\t}"
+                    : "=r"(all)
+                    : "r"((uint32_t)in)
+                    : "memory");
+                if (!all) {
+                    give_up();
+                    break;
+                }
+                s.advance();
+                if (s.on) fetch();
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float v[8];
+                    ckpt_values8(make_uint2(q[u].x, q[u].y), f[u], v);
+                    const uint4 lo = bf16x8_rn(v);
+                    ckpt_values8(make_uint2(q[u].z, q[u].w), f[u], v);
+                    const uint4 hi = bf16x8_rn(v);
+                    // (the odd half first for the upper 64 columns: no two lanes in one bank)
+                    const uint32_t o = dst + (c16 >> 2) * GG_BLOCK;
+                    const int h = c16 >> 2, c = 2 * (c16 & 3);
+                    gg_st16(o + gg_swz(row + 16 * u, c + h), h ? hi : lo);
+                    gg_st16(o + gg_swz(row + 16 * u, c + 1 - h), h ? lo : hi);
+                }
+                gg_fence_async();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0)
+                        mbar_arrive(smem_u32(&sh.tail[stage]));
+                    else
+                        gg_arrive(smem_u32(&sh.peer[stage]), 0);
+                }
+                next_stage();
+            }
+            __syncwarp();
+        }
+        if (MODE == GM_RDX && fix.a.part) {
+            // the parts of dw, from the launch in front
+            const int rows = (fix.a.tiles - fix.a.full) * GG_TILE, w = warp - GG_TAIL_WARP0;
+            const int i = w * gridDim.x + blockIdx.x, all = gridDim.x * GG_TAIL_WARPS;
+            grad_fixup(fix.a, fix.pairs, (int)((long long)rows * i / all), (int)((long long)rows * (i + 1) / all),
+                       sh.slots[w]);
+        }
         if (!Cfg::WGRAD && a.bias.part) {
             for (int b = blockIdx.x; b * 32 < a.bias.E; b += gridDim.x) {
                 grad_bias(a.bias, b, threadIdx.x - 32 * GG_TAIL_WARP0, sh.bias);
@@ -773,72 +948,6 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     tc_fence_after();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-}
-
-// Adds the parts of each split tile in the order of their rows.  CTA (split
-// tile, 8 rows of it).
-__global__ void __launch_bounds__(256) k_grad_fixup(GradArgs a, int pairs) {
-    pdl_begin();
-    const int rem = a.tiles - a.full, i = blockIdx.x, per = a.MT * a.NT;
-    __shared__ int s_slot[GG_MAX_PAIRS], s_n;
-    if (threadIdx.x < 32) {
-        // chunks of all split tiles, of those in front of tile i, and its own
-        const int lane = threadIdx.x;
-        int all = 0, b = 0, own = 0;
-        for (int j = lane; j < rem; j += 32) {
-            int r0, r1;
-            gg_rows(a, (a.full + j) / per, r0, r1);
-            const int n = (gg_steps(r1 - r0) + a.chunk_steps - 1) / a.chunk_steps;
-            all += n;
-            b += j < i ? n : 0;
-            own += j == i ? n : 0;
-        }
-        const long long W = warp_sum(all);
-        b = warp_sum(b);
-        const int e = b + warp_sum(own);
-        // the pairs whose range of chunks meets the tile's, in order
-        int n = 0;
-        for (int p0 = 0; p0 < pairs; p0 += 32) {
-            const int p = p0 + lane, c0 = (int)(W * p / pairs), c1 = (int)(W * (p + 1) / pairs);
-            const bool in = p < pairs && c0 < c1 && c0 < e && c1 > b;
-            const uint32_t m = __ballot_sync(0xffffffffu, in);
-            // (it is a pair's second part where the pair's range begins in an earlier tile)
-            if (in) s_slot[n + __popc(m & ((1u << lane) - 1))] = 2 * p + (c0 < b ? 1 : 0);
-            n += __popc(m);
-        }
-        if (lane == 0) s_n = n;
-    }
-    __syncthreads();
-    const int n = s_n;
-    if (n == 1) return;        // one pair computed the whole tile
-    const int t = a.full + i;
-    int m0, n0;
-    gg_tile(a, t % per, m0, n0);
-    float* out = a.c + ((size_t)(t / per) * a.M + m0) * a.N + n0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int m = blockIdx.y * 8 + (threadIdx.x >> 6) + 4 * h, c = 4 * (threadIdx.x & 63);
-        if (m0 + m >= a.M || n0 + c >= a.N) continue;
-        float4* o = reinterpret_cast<float4*>(out + (size_t)m * a.N + c);
-        const float* p = a.part + m * GG_TILE + c;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p + (size_t)s_slot[j] * (GG_TILE * GG_TILE)));
-            s.x = __fadd_rn(s.x, v.x);
-            s.y = __fadd_rn(s.y, v.y);
-            s.z = __fadd_rn(s.z, v.z);
-            s.w = __fadd_rn(s.w, v.w);
-        }
-        if (a.accumulate) {
-            const float4 v = *o;
-            s.x = __fadd_rn(v.x, s.x);
-            s.y = __fadd_rn(v.y, s.y);
-            s.z = __fadd_rn(v.z, s.z);
-            s.w = __fadd_rn(v.w, s.w);
-        }
-        *o = s;
-    }
 }
 
 // ---- the router's fp32 operands as bf16 parts --------------------------------------
@@ -1081,7 +1190,7 @@ static cudaError_t grad_map(const void* p, CUtensorMapDataType type, long long l
     const cuuint64_t strides[2] = {row, planes > 1 ? row * (cuuint64_t)rows : row};
     const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
     return encode(map, type, 3, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
@@ -1091,9 +1200,11 @@ static cudaError_t bf16_map(const void* p, long long ld, int rows, int cols, int
     return grad_map(p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ld, rows, cols, planes, 64, box_rows, map);
 }
 
+// fix: GM_RDX adds the parts it names; GM_RDW leaves its own there instead of
+// launching k_grad_fixup.
 template <int MODE>
 static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUtensorMap& b_map, void* c,
-                               cudaStream_t st) {
+                               cudaStream_t st, FixupArgs* fix = nullptr) {
     const int grid = grad_grid<MODE>();
     if (grid <= 0) return cudaErrorInvalidConfiguration;
     const int pairs = grid / 2;
@@ -1141,10 +1252,16 @@ static cudaError_t launch_grad(GradArgs a, const CUtensorMap& a_map, const CUten
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, k_grad_gemm<MODE>, a, a_map, b_map, c_map, part_map);
+    const FixupArgs none = {};
+    e = cudaLaunchKernelEx(&cfg, k_grad_gemm<MODE>, a, MODE == GM_RDX ? *fix : none, a_map, b_map, c_map, part_map);
     count_launches(1);
     if (e != cudaSuccess || !split) return e;
-    e = launch_pdl(k_grad_fixup, dim3((unsigned)rem, GG_TILE / 8), dim3(256), 0, st, a, pairs);
+    const FixupArgs f{a, pairs};
+    if (fix) {
+        *fix = f;
+        return e;
+    }
+    e = launch_pdl(k_grad_fixup, dim3((unsigned)(rem * (GG_TILE / 8))), dim3(256), 0, st, f);
     count_launches(1);
     return e;
 }
@@ -1160,7 +1277,7 @@ size_t wgrad_workspace_bytes(int R, int, int K, int) {
 }
 
 struct RouterWs {
-    size_t wp, bias, dlp, xb, part, total;
+    size_t wp, bias, dlp, part, total;
 };
 static RouterWs router_ws(int T, int H, int E) {
     const size_t Ep = align_up(E, 8);
@@ -1169,7 +1286,6 @@ static RouterWs router_ws(int T, int H, int E) {
     L.wp = o; o += align_up(2 * 2 * (size_t)E * H, 256);
     L.bias = o; o += align_up(sizeof(float) * kSplitMaxCtas * (size_t)E, 256);
     L.dlp = o; o += align_up(3 * 2 * (size_t)T * Ep, 256);
-    L.xb = o; o += align_up(2 * (size_t)T * H, 256);
     L.part = o; o += grad_part_bytes(T, GradCfg<GM_RDW>::SPLIT_GAIN);
     L.total = o;
     return L;
@@ -1250,14 +1366,8 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
     s.dlp = (__nv_bfloat16*)(b + L.dlp);
     s.wp = (__nv_bfloat16*)(b + L.wp);
     s.bias_part = db ? (float*)(b + L.bias) : nullptr;
-    s.codes = codes;
-    s.scales = scales;
-    s.items = dw && codes ? (long long)T * (H / 8) : 0;
-    s.K = H;
-    s.xb = (__nv_bfloat16*)(b + L.xb);
     s.flag = flag;
-    e = launch_pdl(k_grad_prepare, dim3((unsigned)(s.dl_ctas + s.w_ctas) + prepare_ctas(s.items)), dim3(kSplitThreads), 0,
-                   st, s);
+    e = launch_pdl(k_grad_prepare, dim3((unsigned)(s.dl_ctas + s.w_ctas)), dim3(kSplitThreads), 0, st, s);
     count_launches(1);
     GradArgs a = {};
     a.G = 1;
@@ -1265,19 +1375,25 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
     a.flag = flag;
     a.wait_ns = wait_ns;
     BiasArgs bias{s.bias_part, s.dl_ctas, E, db, accumulate};
+    FixupArgs fix = {};
     CUtensorMap a_map, b_map;
     if (e == cudaSuccess && dw) {
         e = bf16_map(s.dlp, Ep, T, Ep, 3, GG_K, &a_map);
-        if (e == cudaSuccess) e = bf16_map(x ? x : s.xb, H, T, H, 1, GG_K, &b_map);
+        if (e == cudaSuccess)
+            e = x ? bf16_map(x, H, T, H, 1, GG_K, &b_map)
+                  : grad_map(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, H, T, H, 1, GG_HALF, GG_K, &b_map);
         if (e != cudaSuccess) return e;
         GradArgs d = a;
         d.R = T;
         d.M = E;
         d.accumulate = accumulate;
         d.part = (float*)(b + L.part);
-        d.bias = bias;
-        bias.part = nullptr;
-        e = launch_grad<GM_RDW>(d, a_map, b_map, dw, st);
+        d.x_scales = x ? nullptr : scales;
+        if (!dx) {
+            d.bias = bias;
+            bias.part = nullptr;
+        }
+        e = launch_grad<GM_RDW>(d, a_map, b_map, dw, st, dx ? &fix : nullptr);
     }
     if (e == cudaSuccess && dx) {
         e = bf16_map(s.dlp, Ep, T, Ep, 2, GG_HALF, &a_map);
@@ -1287,7 +1403,7 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
         a.M = T;
         a.bias = bias;
         bias.part = nullptr;
-        e = launch_grad<GM_RDX>(a, a_map, b_map, dx, st);
+        e = launch_grad<GM_RDX>(a, a_map, b_map, dx, st, &fix);
     }
     if (e == cudaSuccess && bias.part) {
         e = launch_pdl(k_router_bias, dim3((unsigned)((E + 31) / 32)), dim3(128), 0, st, bias);
