@@ -59,6 +59,23 @@ __device__ __forceinline__ float4 rs_load4(const float* __restrict__ p, int cols
     return v;
 }
 
+// Two sums at once: a fused multiply-add each (Blackwell's packed form).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 rs_twice(float v) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void rs_fma2(f32x2& acc, f32x2 a, f32x2 b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ float4 rs_four(f32x2 a, f32x2 b) {
+    float4 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(a));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.z), "=f"(v.w) : "l"(b));
+    return v;
+}
+
 // (all of a thread's loads of a round are issued before the first is stored)
 __global__ void __launch_bounds__(RS_THREADS) k_router_grad_small(RouterSmallArgs a) {
     pdl_begin();
@@ -73,7 +90,8 @@ __global__ void __launch_bounds__(RS_THREADS) k_router_grad_small(RouterSmallArg
         // experts 4 (tid / 16) .. + 3, columns 4 (tid % 16) .. + 3
         const int me = 4 * (tid >> 4), mc = 4 * (tid & 15);
         const bool sums = a.db && h0 == 0 && tid < RS_WE && e0 + tid < a.E;
-        float acc[4][4] = {}, bias = 0.0f;
+        f32x2 acc[4][2] = {};
+        float bias = 0.0f;
         float4 d[ND];
         uint4 xq[NX];
         uint32_t xf[NX];
@@ -129,14 +147,13 @@ __global__ void __launch_bounds__(RS_THREADS) k_router_grad_small(RouterSmallArg
 #pragma unroll 8
                 for (int t = 0; t < n; ++t) {
                     const float4 dl = *reinterpret_cast<const float4*>(&s.d[t][me]);
-                    const float4 v = *reinterpret_cast<const float4*>(&s.x[t][mc]);
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&s.x[t][mc]);
                     const float dv[4] = {dl.x, dl.y, dl.z, dl.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        acc[i][0] = fmaf(dv[i], v.x, acc[i][0]);
-                        acc[i][1] = fmaf(dv[i], v.y, acc[i][1]);
-                        acc[i][2] = fmaf(dv[i], v.z, acc[i][2]);
-                        acc[i][3] = fmaf(dv[i], v.w, acc[i][3]);
+                        const f32x2 two = rs_twice(dv[i]);
+                        rs_fma2(acc[i][0], two, v.x);
+                        rs_fma2(acc[i][1], two, v.y);
                     }
                 }
         }
@@ -149,7 +166,7 @@ __global__ void __launch_bounds__(RS_THREADS) k_router_grad_small(RouterSmallArg
         for (int i = 0; i < 4; ++i)
             if (e0 + me + i < a.E && h0 + mc < a.H) {
                 float4* o = reinterpret_cast<float4*>(a.dw + (size_t)(e0 + me + i) * a.H + h0 + mc);
-                float4 v = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                float4 v = rs_four(acc[i][0], acc[i][1]);
                 if (a.accumulate) {
                     const float4 b = *o;
                     v = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
@@ -164,7 +181,7 @@ __global__ void __launch_bounds__(RS_THREADS) k_router_grad_small(RouterSmallArg
     // group g = tid / 64: experts RS_XE / 4 g .. of a round; in it tokens
     // (tid / 8 % 8) + 8 i, columns 4 (tid % 8) .. + 3
     const int g = tid >> 6, dt = (tid >> 3) & 7, dc = 4 * (tid & 7);
-    float acc[4][4] = {};
+    f32x2 acc[4][2] = {};
     for (int e0 = 0; e0 < a.E; e0 += RS_XE) {
         const int n = min(RS_XE, a.E - e0), n4 = (n + 3) & ~3;      // (what lies behind n is zeros)
         if (e0) __syncthreads();
@@ -196,19 +213,18 @@ __global__ void __launch_bounds__(RS_THREADS) k_router_grad_small(RouterSmallArg
         const int lo = g * (RS_XE / 4), hi = min(n4, lo + RS_XE / 4);
 #pragma unroll 2
         for (int e = lo; e < hi; e += 4) {
-            float4 v[4];
+            ulonglong2 v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float4*>(&s.w[e + j][dc]);
+            for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const ulonglong2*>(&s.w[e + j][dc]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 d = *reinterpret_cast<const float4*>(&s.d[dt + 8 * i][e]);
                 const float dv[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    acc[i][0] = fmaf(dv[j], v[j].x, acc[i][0]);
-                    acc[i][1] = fmaf(dv[j], v[j].y, acc[i][1]);
-                    acc[i][2] = fmaf(dv[j], v[j].z, acc[i][2]);
-                    acc[i][3] = fmaf(dv[j], v[j].w, acc[i][3]);
+                    const f32x2 two = rs_twice(dv[j]);
+                    rs_fma2(acc[i][0], two, v[j].x);
+                    rs_fma2(acc[i][1], two, v[j].y);
                 }
             }
         }
@@ -217,7 +233,7 @@ __global__ void __launch_bounds__(RS_THREADS) k_router_grad_small(RouterSmallArg
     __syncthreads();
     float4(*part)[RS_XT][RS_XH / 4] = reinterpret_cast<float4(*)[RS_XT][RS_XH / 4]>(rs_raw);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[g][dt + 8 * i][tid & 7] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    for (int i = 0; i < 4; ++i) part[g][dt + 8 * i][tid & 7] = rs_four(acc[i][0], acc[i][1]);
     __syncthreads();
     const int t = tid >> 3;
     if (t0 + t < a.T) {
