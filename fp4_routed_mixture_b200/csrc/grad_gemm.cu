@@ -49,6 +49,7 @@
 // burst and 0.47 in a loop of seconds (cuBLAS there 0.39-0.415); 16 groups of
 // 1726 rows on average, 4096 x 4096: 0.70 ms (1.3 PFLOP/s), bound by the tensor
 // cores beside 1.07 GB of results.
+#include "bf16_parts.cuh"
 #include "ckpt.cuh"
 #include "kernels.cuh"
 #include "moe_common.cuh"
@@ -950,18 +951,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// ---- the router's fp32 operands as bf16 parts --------------------------------------
-// v = h + m + l, each with 8 significant bits: h and m rounded to nearest, l
-// exact (24 = 8 + 8 + 8 bits).  An infinity or NaN is its own first part.
-__device__ __forceinline__ void split3(float v, float& h, float& m, float& l) {
-    h = __bfloat162float(__float2bfloat16_rn(v));
-    // (a finite value that rounds up to infinity is truncated instead)
-    if (fabsf(h) == INFINITY) h = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-    const float r = h == v ? 0.0f : v - h;
-    m = __bfloat162float(__float2bfloat16_rn(r));
-    l = m == r ? 0.0f : r - m;
-}
-
+// ---- what the products need as bf16 ----------------------------------------------------
 constexpr int kSplitThreads = 256;
 constexpr int kSplitMaxCtas = 148 * 4;
 

@@ -236,14 +236,15 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
                               const int32_t* offsets, const int32_t* perm, int k, int R, int rows, int N, int K, int G,
                               float* dw, int accumulate, void* ws, uint64_t wait_ns, int withhold, cudaStream_t st);
 size_t router_backward_workspace_bytes(int T, int H, int E);
-// Calls that run on the CUDA cores (router_grad_small.cu) instead of the tensor
-// cores: at most 128 tokens, or 256 with at most 2^27 multiply-adds a product.
-// Measured (us, CUDA cores / tensor cores; H, experts): 64 tokens 1024, 64 4.1 /
-// 13.7 and 4096, 256 12.0 / 20.8; 128 tokens 6.8 / 15.0 and 21.6 / 22.0; 256
-// tokens 1024, 256 18.0 / 21.4, 512, 1024 21.5 / 40.0, 4096, 64 17.5 / 20.4, but
-// 4096, 256 37 / 24; 512 tokens 1024, 64 23.8 / 20.3.
+// Calls that take one launch (router_grad_small.cu) instead of three
+// (grad_gemm.cu): at most 512 tokens and 2^28 multiply-adds a product.  Measured
+// (us, one launch / three; H, experts): 64 tokens 1024, 64 3.7 / 14.3 and 4096, 256
+// 8.9 / 21.1; 256 tokens 4096, 256 22.1 / 24.7, 512, 1024 20.9 / 40.5; 512 tokens
+// 1024, 64 19.9 / 21.1, 4096, 64 23.2 / 23.6, 512, 1024 29.1 / 44.5; but 768 tokens
+// 1024, 64 30.1 / 22.2, and above 2^28 384 tokens 4096, 256 30.9 / 26.9, 128 tokens
+// 4096, 1024 46.9 / 43.3.
 inline bool router_grad_small(int T, int H, int E) {
-    return T <= 128 || (T <= 256 && (long long)T * H * E <= 1LL << 27);
+    return T <= 512 && (long long)T * H * E <= 1LL << 28;
 }
 cudaError_t launch_router_grad_small(const float* dl, const void* x, const uint8_t* codes, const uint8_t* scales,
                                      const float* w, int T, int H, int E, void* dx, float* dw, float* db,

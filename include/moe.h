@@ -375,9 +375,8 @@ int moe_route_backward(const float *logits, const int32_t *topk_idx, const float
  * being NULL; neither is needed when dw is NULL.  w_router is needed for dx.
  * accumulate 1 adds dw and dbias to what is there (dx is always overwritten;
  * sums below 2^-126 may become 0).
- * Small calls (up to 128 tokens, or 256) use fp32 multiply-adds.  Larger ones form the
- * products of fp32 operands from bf16 parts on the tensor cores, accumulated in
- * fp32: dw from all three parts of dlogits (exact), dx from the leading two
+ * The products of fp32 operands are formed from bf16 parts on the tensor cores,
+ * accumulated in fp32: dw from all three parts of dlogits (exact), dx from the leading two
  * parts of each operand (about 16 bits, before its rounding to 8).  An infinity
  * in dlogits, x or w_router makes the sums it enters infinite or NaN (in parts,
  * infinity times a part of 0 is NaN).

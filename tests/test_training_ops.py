@@ -235,6 +235,9 @@ def pow2_rows(x):
     (1500, 256, 5, "bf16"), (1100, 512, 513, "ckpt"),
     (128, 96, 70, "bf16"), (129, 2048, 600, "bf16"), (256, 1024, 512, "ckpt"), (256, 1056, 512, "bf16"),
     (257, 32, 1, "bf16"), (300, 96, 3, "bf16"), (290, 32, 7, "bf16"), (320, 128, 65, "ckpt"), (200, 256, 100, "ckpt"),
+    (512, 1024, 512, "ckpt"), (511, 1056, 510, "bf16"), (512, 1152, 512, "ckpt"), (513, 32, 1, "bf16"),
+    (513, 128, 3, "ckpt"),
+    (512, 64, 130, "bf16"), (700, 384, 70, "ckpt"), (640, 896, 300, "ckpt"), (1030, 128, 9, "ckpt"),
 ])
 def test_router_backward(moe, T, H, E, kind):
     r = np.random.default_rng(T + H + E)
@@ -281,6 +284,33 @@ def test_router_backward_wide_range(moe, T):
     d64, x = dl.astype(np.float64), host(xb).astype(np.float64)
     close(host(dw), d64.T @ x, (3 * T + 8) * 2 * U * (np.abs(d64).T @ np.abs(x)), "dw")
     close(host(db), d64.sum(0), (T + 8) * U * np.abs(d64).sum(0), "dbias")
+
+
+@pytest.mark.parametrize("T,E", [(40, 17), (300, 100), (600, 70), (1300, 300)])
+def test_router_backward_not_finite(moe, T, E):
+    """A NaN or infinity in dlogits, or in a checkpoint, reaches the sums that hold
+    it and no others."""
+    r = np.random.default_rng(T)
+    H = 384
+    dl = (1e-3 * r.standard_normal((T, E))).astype(np.float32)
+    xb = bf16(r.standard_normal((T, H)))
+    w = (0.02 * r.standard_normal((E, H))).astype(np.float32)
+    codes, scales = moe.moe_ckpt_pack(xb)
+    clean = moe.moe_router_logits_backward(cu(dl), cu(w), codes=codes, scales=scales)
+    bad = dl.copy()
+    bad[3, 5] = np.nan
+    bad[T - 1, E - 1] = np.inf
+    codes[T // 2, 7] = 0x7F
+    codes[T - 2, H - 1] = 0xFF
+    scales[1, 1] = 255
+    dx, dw, db = moe.moe_router_logits_backward(cu(bad), cu(w), codes=codes, scales=scales)
+    rows, cols = np.isin(np.arange(E), (5, E - 1)), np.isin(np.arange(H), (7, H - 1)) | (np.arange(H) // 128 == 1)
+    hit = torch.from_numpy(rows[:, None] | cols[None]).cuda()
+    assert not torch.isfinite(dw[hit]).any() and torch.equal(dw[~hit], clean[1][~hit])
+    hit = torch.from_numpy(rows).cuda()
+    assert not torch.isfinite(db[hit]).any() and torch.equal(db[~hit], clean[2][~hit])
+    hit = torch.from_numpy(np.isin(np.arange(T), (3, T - 1))).cuda()
+    assert not torch.isfinite(dx[hit]).any() and torch.equal(dx[~hit], clean[0][~hit])
 
 
 def test_router_backward_no_tokens(moe):
