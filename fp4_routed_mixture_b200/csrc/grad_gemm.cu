@@ -1013,19 +1013,17 @@ __global__ void __launch_bounds__(kSplitThreads) k_grad_prepare(PrepareArgs a) {
                     for (int j = 0; j < 4; ++j)
                         if (c + j < a.E) v[j] = __ldg(p + j);
                 }
-                float h[4], m[4], l[4];
+                uint2 h, m, l;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sum[j] += v[j];
-                    split3(v[j], h[j], m[j], l[j]);
-                }
+                for (int j = 0; j < 4; ++j) sum[j] += v[j];
+                split3x2(v[0], v[1], h.x, m.x, l.x);
+                split3x2(v[2], v[3], h.y, m.y, l.y);
                 if (a.parts) {
                     __nv_bfloat16* o = a.dlp + (size_t)t * a.Ep + c;
                     const size_t plane = (size_t)a.T * a.Ep;
-                    *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(h[0], h[1]), bf16x2_rn(h[2], h[3]));
-                    *reinterpret_cast<uint2*>(o + plane) = make_uint2(bf16x2_rn(m[0], m[1]), bf16x2_rn(m[2], m[3]));
-                    if (a.parts == 3)
-                        *reinterpret_cast<uint2*>(o + 2 * plane) = make_uint2(bf16x2_rn(l[0], l[1]), bf16x2_rn(l[2], l[3]));
+                    *reinterpret_cast<uint2*>(o) = h;
+                    *reinterpret_cast<uint2*>(o + plane) = m;
+                    if (a.parts == 3) *reinterpret_cast<uint2*>(o + 2 * plane) = l;
                 }
             }
         }
@@ -1051,13 +1049,11 @@ __global__ void __launch_bounds__(kSplitThreads) k_grad_prepare(PrepareArgs a) {
         const size_t n4 = (size_t)a.E * a.H / 4, step = (size_t)a.w_ctas * kSplitThreads;
         for (size_t i = (size_t)b * kSplitThreads + threadIdx.x; i < n4; i += step) {
             const float4 v = __ldg(reinterpret_cast<const float4*>(a.w) + i);
-            float h[4], m[4], l;
-            split3(v.x, h[0], m[0], l);
-            split3(v.y, h[1], m[1], l);
-            split3(v.z, h[2], m[2], l);
-            split3(v.w, h[3], m[3], l);
-            reinterpret_cast<uint2*>(a.wp)[i] = make_uint2(bf16x2_rn(h[0], h[1]), bf16x2_rn(h[2], h[3]));
-            reinterpret_cast<uint2*>(a.wp)[n4 + i] = make_uint2(bf16x2_rn(m[0], m[1]), bf16x2_rn(m[2], m[3]));
+            uint2 h, m, l;
+            split3x2(v.x, v.y, h.x, m.x, l.x);
+            split3x2(v.z, v.w, h.y, m.y, l.y);
+            reinterpret_cast<uint2*>(a.wp)[i] = h;
+            reinterpret_cast<uint2*>(a.wp)[n4 + i] = m;
         }
         return;
     }
