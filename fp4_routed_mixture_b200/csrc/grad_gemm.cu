@@ -12,12 +12,15 @@
 //   GM_RDX     r = experts, A = dlogits, B = w_router, both fp32 with a bf16
 //              result: the leading two parts of each, three products (the
 //              smallest, low x low, is below 2^-16 of the terms)
-// k_grad_prepare writes what is not bf16 as bf16 to the workspace first: the
-// checkpoint's values and the fp32 operands' parts.  Conversion inside the GEMM
-// (converter warps between a copy of the codes and the MMA) was built and
-// measured: it needs about 750 issue cycles per stage and scheduler against the
-// 512 of the stage's MMAs, 424 TFLOP/s in all (16384 x 4096 x 4096), where the
-// conversion in front costs 3 bytes of traffic per value.
+// k_grad_prepare writes fp32 operands' parts, and in GM_WGRAD the checkpoint's
+// values, as bf16 to the workspace first.  Where a stage takes longer than about
+// 1500 cycles anyway, four warps convert the codes between their copy and the MMA
+// (GM_.._CODES): in dW of the router, three products a stage (16384 tokens, H 4096,
+// 256 experts, with dx: 217 us with the values in the workspace, 187 without), and
+// with few rows, where C's stores bound (16 groups of 20 rows on average, 4096 x 4096:
+// 202 us / 176).  In GM_WGRAD a stage's MMAs take 512 cycles: 750 us for 16384 x 4096 x
+// 4096, where the conversion in front costs 3 bytes of traffic per value and 30 us
+// of 465.
 //
 // One SM pair (cluster of two CTAs, tcgen05 cta_group::2) per 256 x 256 tile of
 // C: the CTA of rank q supplies columns 128 q .. + 127 of A's and of B's tile
@@ -26,8 +29,8 @@
 //                 contraction runs over smem rows, except A of GM_RDX)
 //   warp 1        (leader CTA) issues the MMAs
 //   warp 2        GM_WGRAD through perm: checks the table
-//   warps 4-7     GM_WGRAD: clear the rows behind a group's last one; else the
-//                 sums of dbias
+//   warps 4-7     GM_.._CODES: codes to bf16.  GM_WGRAD: clear the rows behind a
+//                 group's last one.  Router: the parts of split tiles, dbias
 //   warps 8-15    epilogue, from two 256-column accumulators in TMEM
 // Work: pair p takes the tiles p, p + P, ... of the first floor(tiles / P) P
 // ones whole; the remaining tiles are cut so that the last round is not left to
@@ -57,8 +60,9 @@
 
 namespace moe {
 
-// (GM_WGRAD_FEW: GM_WGRAD for few rows, where storing C is what takes the time)
-enum { GM_WGRAD = 0, GM_RDW = 1, GM_RDX = 2, GM_WGRAD_FEW = 3 };
+// (GM_WGRAD_FEW: GM_WGRAD for few rows, where storing C is what takes the time.
+// GM_.._CODES: B is read as a checkpoint's codes, which the kernel makes bf16)
+enum { GM_WGRAD = 0, GM_RDW = 1, GM_RDX = 2, GM_WGRAD_FEW = 3, GM_RDW_CODES = 4, GM_WGRAD_CODES = 5 };
 
 constexpr int GG_TILE = 256;            // rows and columns of C per pair
 constexpr int GG_HALF = 128;            // per CTA: rows of A's tile, columns of B's
@@ -80,23 +84,32 @@ static_assert(2 * GG_REGS_LOAD + 2 * GG_REGS_EPI <= 4 * GG_REGS, "registers of t
 // other form; N = K = 4096): 40 rows 18.0 / 21.7, 128 19.0 / 22.5, 256 20.9 / 23.2,
 // 512 27.2 / 26.3; 16 groups of 100 rows 222 / 219, of 400 326 / 268, of 800 486 / 467.
 constexpr int kFewRows = 256;
+// Up to this many rows a group, without perm, the kernel reads the codes itself
+// (us, GM_WGRAD_CODES / in front; 4096 x 4096: 40 rows 17.6 / 17.6, 128 19.1 / 18.9, 192
+// 21.7 / 19.9; 16 groups of 60 rows on average 190 / 213, of 100 198 / 221, of 128 217 / 222;
+// 64 rows, 16384 x 4096: 49 / 56; and one launch).
+constexpr int kConvertRows = 128;
+static_assert(kConvertRows <= kFewRows, "the form that converts");
 
 template <int MODE>
 struct GradCfg {
-    static constexpr bool WGRAD = MODE == GM_WGRAD || MODE == GM_WGRAD_FEW;
-    static constexpr int AP = WGRAD ? 1 : MODE == GM_RDW ? 3 : 2;   // parts of A
+    static constexpr bool CODES = MODE == GM_RDW_CODES || MODE == GM_WGRAD_CODES;
+    static constexpr bool FEW = MODE == GM_WGRAD_FEW || MODE == GM_WGRAD_CODES;
+    static constexpr bool WGRAD = MODE == GM_WGRAD || FEW;
+    static constexpr bool RDW = MODE == GM_RDW || MODE == GM_RDW_CODES;
+    static constexpr int AP = WGRAD ? 1 : RDW ? 3 : 2;   // parts of A
     static constexpr int BP = MODE == GM_RDX ? 2 : 1;
     static constexpr int OPS = (AP + BP) * GG_PLANE;
     // Stages, and pieces of 4 KB that an epilogue warp has on their way out.
-    static constexpr int STAGES = MODE == GM_WGRAD ? 6 : MODE == GM_WGRAD_FEW ? 5 : 3;
-    static constexpr int OUTS = MODE == GM_WGRAD_FEW ? 2 : 1;
-    static constexpr int ACC_STEPS = WGRAD ? 16 : MODE == GM_RDW ? 4 : 16;
+    static constexpr int STAGES = FEW ? 5 : WGRAD ? 6 : 3;
+    static constexpr int OUTS = FEW ? 2 : 1;
+    static constexpr int ACC_STEPS = RDW ? 4 : 16;
     // Largest chunk of a split tile, and what splitting has to save, in stages
     // (about 5 us, what k_grad_fixup adds: a stage takes 0.28 us in GM_WGRAD, 0.85 with
     // three products; 512 tokens, 8 stages in 2: the same time with and without).  A
     // result of GM_RDX, of at most 16 stages, is not split.
     static constexpr int CHUNK_STEPS = WGRAD ? 16 : 8;
-    static constexpr int SPLIT_GAIN = WGRAD ? 18 : MODE == GM_RDW ? 8 : 1 << 20;
+    static constexpr int SPLIT_GAIN = WGRAD ? 18 : RDW ? 8 : 1 << 20;
 };
 
 template <int MODE>
@@ -156,7 +169,7 @@ struct GradArgs {
     float* c;                  // (GM_RDX stores through its map alone)
     int accumulate;
     float* part;               // [pairs][2][256][256]
-    const uint8_t* x_scales;   // GM_RDW: B is a checkpoint's codes with these scales, or NULL
+    const uint8_t* x_scales;   // GM_.._CODES
     BiasArgs bias;             // GM_RDW, GM_RDX
     int32_t* flag;
     uint64_t wait_ns;
@@ -310,6 +323,15 @@ __device__ __forceinline__ void gg_rows(const GradArgs& a, int g, int& r0, int& 
         r0 = min(max(__ldg(a.offsets + g), 0), a.R);
         r1 = min(max(__ldg(a.offsets + g + 1), r0), a.R);
     }
+}
+// Of the groups i, i + n, ..: one does not ascend within [0, R].
+__device__ __forceinline__ bool bad_offsets(const int32_t* offsets, int G, int R, int i, int n) {
+    bool bad = false;
+    for (int g = i; g < G; g += n) {
+        const int b = __ldg(offsets + g), e = __ldg(offsets + g + 1);
+        bad |= b < 0 || e < b || e > R;
+    }
+    return bad;
 }
 // Tile i of a group, row by row.  (Bands of 4 or 8 columns, which would share
 // both operands' panels in L2 among the tiles in flight, measured the same.)
@@ -564,7 +586,6 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         *abort = 1;
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(gg_peer(smem_u32(&sh.abort), rank ^ 1u)), "r"(1u)
                      : "memory");
-        raise_flag(a.flag, FLAG_TIMEOUT);
     };
     auto wait = [&](uint32_t bar, uint32_t parity) { return gg_wait(bar, parity, a.wait_ns, abort); };
     // of a whole warp: its lanes go on or give up together
@@ -574,7 +595,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     // The waits for what is in flight are not cut short: 0.1 s at the least.
     const uint64_t drain_ns = max(a.wait_ns, (uint64_t)100000000);
     auto final_wait = [&](uint32_t bar, uint32_t parity) {
-        if (!gg_wait(bar, parity, drain_ns, nullptr)) raise_flag(a.flag, FLAG_TIMEOUT);
+        if (!gg_wait(bar, parity, drain_ns, nullptr)) *abort = 1;
     };
     const Walk walk0(a, sh.rem_pre, pair, pairs);
     int stage = 0;
@@ -595,8 +616,9 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     auto has_tail = [&](const Segment& s, int st) {
         return Cfg::WGRAD && s.r1 < a.R && s.r1 - s.r0 - st * GG_K < GG_K;
     };
-    // B comes as a checkpoint's codes, which warps 4-7 turn into bf16.
-    const bool convert = MODE == GM_RDW && a.x_scales;
+    constexpr bool CODES = Cfg::CODES;
+    // No kernel in front has cleared the error word and checked the offsets.
+    constexpr bool FIRST = MODE == GM_WGRAD_CODES;
     auto next_parity = [&](uint32_t& bits) {
         const uint32_t p = bits >> stage & 1u;
         bits ^= 1u << stage;
@@ -611,7 +633,8 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             // waits here run to their limit even when another role has given
             // up: "empty" reaches both CTAs, so both have then issued the same
             // stages, and the leader's last waits cover the copies of both.)
-            const uint32_t bytes = (convert ? AP : AP + BP) * GG_PLANE;
+            const uint32_t bytes = (CODES ? AP : AP + BP) * GG_PLANE;
+            constexpr uint32_t code_bytes = GG_K * GG_HALF;
             bool first = true;
             for (Steps s(walk0); s.on; s.advance()) {
                 if (!gg_wait(smem_u32(&sh.empty[stage]), phase ^ 1u, drain_ns, nullptr)) {
@@ -625,9 +648,18 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                 }
                 const bool tail = has_tail(s.seg, s.st);
                 uint32_t bar = smem_u32(tail ? &sh.tail_landed[stage] : &sh.landed[stage]);
-                if (rank == 0 || tail) {
-                    mbar_expect_tx(bar, tail ? bytes : 2 * bytes);
-                    next_parity(tail ? tails : lands);
+                if (CODES) {
+                    mbar_expect_tx(smem_u32(&sh.tail_landed[stage]), code_bytes + (tail ? bytes : 0));
+                    next_parity(tails);
+                }
+                if (tail) {
+                    if (!CODES) {
+                        mbar_expect_tx(bar, bytes);
+                        next_parity(tails);
+                    }
+                } else if (rank == 0) {
+                    mbar_expect_tx(bar, 2 * bytes);
+                    next_parity(lands);
                 } else {
                     bar = gg_peer(bar, 0);
                 }
@@ -643,12 +675,9 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                         gg_tma(dst + GG_BLOCK, &a_map, m + 64, r, p, bar);
                     }
                 }
-                if (convert) {
+                if (CODES) {
                     // 128 codes of each row, where their values will be
-                    bar = smem_u32(&sh.tail_landed[stage]);
-                    mbar_expect_tx(bar, GG_K * GG_HALF);
-                    next_parity(tails);
-                    gg_tma(dst, &b_map, n, r, 0, bar);
+                    gg_tma(dst, &b_map, n, r, 0, smem_u32(&sh.tail_landed[stage]));
                 } else {
 #pragma unroll
                     for (int p = 0; p < BP; ++p, dst += GG_PLANE) {
@@ -684,14 +713,11 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                         tc_fence_after();
                         const uint32_t d = tmem + buf * GG_TILE;
                         for (int s = st; s < st1; ++s) {
-                            bool in;
-                            if (has_tail(seg, s)) {
+                            const bool tail = has_tail(seg, s);
+                            bool in = tail || wait(smem_u32(&sh.landed[stage]), next_parity(lands));
+                            if (tail || CODES) {
                                 const uint32_t p = next_parity(tails);
-                                in = wait(smem_u32(&sh.tail[stage]), p) && wait(smem_u32(&sh.peer[stage]), p);
-                            } else {
-                                const uint32_t p = next_parity(lands);
-                                in = wait(smem_u32(&sh.landed[stage]), p) &&
-                                     (!convert || (wait(smem_u32(&sh.tail[stage]), p) && wait(smem_u32(&sh.peer[stage]), p)));
+                                in = in && wait(smem_u32(&sh.tail[stage]), p) && wait(smem_u32(&sh.peer[stage]), p);
                             }
                             if (!in) {
                                 give_up();
@@ -711,7 +737,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                             };
                             if constexpr (Cfg::WGRAD) {
                                 product(0, 0, true);
-                            } else if constexpr (MODE == GM_RDW) {
+                            } else if constexpr (Cfg::RDW) {
                                 product(2, 0, true);
                                 product(1, 0, false);
                                 product(0, 0, false);
@@ -734,6 +760,12 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             }
             // every MMA is done before either CTA frees its TMEM
             final_wait(smem_u32(&sh.drain), 0);
+        } else if (Cfg::WGRAD && warp == 2 && FIRST) {
+            if (blockIdx.x == 0) {
+                if (lane == 0) *a.flag = 0;
+                __syncwarp();
+                if (a.offsets && bad_offsets(a.offsets, a.G, a.R, lane, 32)) raise_flag(a.flag, FLAG_BOUNDS);
+            }
         } else if (Cfg::WGRAD && warp == 2 && a.perm) {
             // (k_grad_prepare reads row 0 for a bad entry; the error word is this
             // call's only from the second kernel on)
@@ -750,7 +782,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         __syncwarp();
     } else if (warp < GG_EPI_WARP0) {
         gg_regs_down<GG_REGS_LOAD>();
-        if (convert) {
+        if constexpr (CODES) {
             // ---------------- codes to bf16 ----------------
             // 64 rows of 128 codes, 16 at a time: thread t takes columns 16 (t % 8)
             // .. of rows t / 8 + 16 u.  The values go where the codes were.
@@ -767,7 +799,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             if (s.on) fetch();
             while (s.on) {
                 const bool in = warp_wait(smem_u32(&sh.tail_landed[stage]), next_parity(tails));
-                const uint32_t dst = smem_u32(sh.ops[stage]) + AP * GG_PLANE;
+                const uint32_t ops = smem_u32(sh.ops[stage]), dst = ops + AP * GG_PLANE;
                 uint4 q[4];
                 float f[4];
 #pragma unroll
@@ -791,15 +823,21 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                     give_up();
                     break;
                 }
+                // (rows behind the group's last one: see below)
+                const int valid = has_tail(s.seg, s.st) ? s.seg.r1 - s.seg.r0 - s.st * GG_K : GG_K;
                 s.advance();
                 if (s.on) fetch();
+                if (valid < GG_K)
+                    for (int i = t; i < AP * GG_PLANE / 16; i += 32 * GG_TAIL_WARPS)
+                        if ((i >> 3 & (GG_K - 1)) >= valid) gg_st16(ops + i * 16, make_uint4(0u, 0u, 0u, 0u));
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     float v[8];
                     ckpt_values8(make_uint2(q[u].x, q[u].y), f[u], v);
-                    const uint4 lo = bf16x8_rn(v);
+                    uint4 lo = bf16x8_rn(v);
                     ckpt_values8(make_uint2(q[u].z, q[u].w), f[u], v);
-                    const uint4 hi = bf16x8_rn(v);
+                    uint4 hi = bf16x8_rn(v);
+                    if (row + 16 * u >= valid) lo = hi = make_uint4(0u, 0u, 0u, 0u);
                     // (the odd half first for the upper 64 columns: no two lanes in one bank)
                     const uint32_t o = dst + (c16 >> 2) * GG_BLOCK;
                     const int h = c16 >> 2, c = 2 * (c16 & 3);
@@ -831,7 +869,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
         }
-        if (Cfg::WGRAD && a.offsets) {
+        if (Cfg::WGRAD && a.offsets && !CODES) {
             // ---------------- rows behind a group's last one ----------------
             const int t = threadIdx.x - 32 * GG_TAIL_WARP0;
             for (Steps s(walk0); s.on; s.advance()) {
@@ -946,6 +984,12 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     gg_cluster_sync();      // no remote arrive or MMA targets this CTA any more
+    if (threadIdx.x == 0 && *abort) {
+        // (not before CTA 0 has cleared the word: it starts first, and 10 ms is long)
+        const uint64_t t0 = global_ns();
+        while (FIRST && global_ns() - t0 < 10000000) __nanosleep(10000);
+        raise_flag(a.flag, FLAG_TIMEOUT);
+    }
     tc_fence_after();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
@@ -984,11 +1028,7 @@ struct PrepareArgs {
 __global__ void __launch_bounds__(kSplitThreads) k_grad_prepare(PrepareArgs a) {
     pdl_begin();
     if (blockIdx.x == 0) {
-        bool bad = false;
-        if (a.offsets)
-            for (int g = threadIdx.x; g < a.G; g += kSplitThreads)
-                bad |= a.offsets[g] < 0 || a.offsets[g + 1] < a.offsets[g] || a.offsets[g + 1] > a.R;
-        bad = __syncthreads_or(bad);
+        const bool bad = __syncthreads_or(a.offsets && bad_offsets(a.offsets, a.G, a.R, threadIdx.x, kSplitThreads));
         if (threadIdx.x == 0) *a.flag = bad ? FLAG_BOUNDS : 0;
     }
     int b = blockIdx.x;
@@ -1283,25 +1323,31 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
                               float* dw, int accumulate, void* ws, uint64_t wait_ns, int withhold, cudaStream_t st) {
     int32_t* flag = (int32_t*)ws;
     cudaError_t e = cudaSuccess;
-    PrepareArgs s = {};
-    s.codes = codes;
-    s.scales = scales;
-    s.items = (long long)R * (K / 8);
-    s.K = K;
-    s.perm = perm;
-    s.k_div = k;
-    s.xrows = rows;
-    s.xb = (__nv_bfloat16*)((char*)ws + 256);
-    s.offsets = offsets;
-    s.G = G;
-    s.R = R;
-    s.flag = flag;
-    e = launch_pdl(k_grad_prepare, dim3(std::max(1u, prepare_ctas(s.items))), dim3(kSplitThreads), 0, st, s);
-    count_launches(1);
-    if (e == cudaSuccess && R == 0) return accumulate ? e : cudaMemsetAsync(dw, 0, sizeof(float) * G * N * K, st);
+    __nv_bfloat16* xb = (__nv_bfloat16*)((char*)ws + 256);
+    const bool convert = R > 0 && !perm && R / G <= kConvertRows;
+    if (!convert) {
+        PrepareArgs s = {};
+        s.codes = codes;
+        s.scales = scales;
+        s.items = (long long)R * (K / 8);
+        s.K = K;
+        s.perm = perm;
+        s.k_div = k;
+        s.xrows = rows;
+        s.xb = xb;
+        s.offsets = offsets;
+        s.G = G;
+        s.R = R;
+        s.flag = flag;
+        e = launch_pdl(k_grad_prepare, dim3(std::max(1u, prepare_ctas(s.items))), dim3(kSplitThreads), 0, st, s);
+        count_launches(1);
+        if (e == cudaSuccess && R == 0) return accumulate ? e : cudaMemsetAsync(dw, 0, sizeof(float) * G * N * K, st);
+    }
     CUtensorMap a_map, b_map;
     if (e == cudaSuccess) e = bf16_map(dy, lddy, R, N, 1, GG_K, &a_map);
-    if (e == cudaSuccess) e = bf16_map(s.xb, K, R, K, 1, GG_K, &b_map);
+    if (e == cudaSuccess)
+        e = convert ? grad_map(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, K, R, K, 1, GG_HALF, GG_K, &b_map)
+                    : bf16_map(xb, K, R, K, 1, GG_K, &b_map);
     if (e != cudaSuccess) return e;
     GradArgs a = {};
     a.offsets = offsets;
@@ -1317,7 +1363,9 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
     a.flag = flag;
     a.wait_ns = wait_ns;
     a.withhold = withhold;
+    a.x_scales = scales;
     // (rows of a group: the average stands for them)
+    if (convert) return launch_grad<GM_WGRAD_CODES>(a, a_map, b_map, dw, st);
     return R / G <= kFewRows ? launch_grad<GM_WGRAD_FEW>(a, a_map, b_map, dw, st)
                              : launch_grad<GM_WGRAD>(a, a_map, b_map, dw, st);
 }
@@ -1374,12 +1422,13 @@ cudaError_t launch_router_backward(const float* dl, const void* x, const uint8_t
         d.M = E;
         d.accumulate = accumulate;
         d.part = (float*)(b + L.part);
-        d.x_scales = x ? nullptr : scales;
+        d.x_scales = scales;
         if (!dx) {
             d.bias = bias;
             bias.part = nullptr;
         }
-        e = launch_grad<GM_RDW>(d, a_map, b_map, dw, st, dx ? &fix : nullptr);
+        e = x ? launch_grad<GM_RDW>(d, a_map, b_map, dw, st, dx ? &fix : nullptr)
+              : launch_grad<GM_RDW_CODES>(d, a_map, b_map, dw, st, dx ? &fix : nullptr);
     }
     if (e == cudaSuccess && dx) {
         e = bf16_map(s.dlp, Ep, T, Ep, 2, GG_HALF, &a_map);
