@@ -313,6 +313,19 @@ def test_router_backward_not_finite(moe, T, E):
     assert not torch.isfinite(dx[hit]).any() and torch.equal(dx[~hit], clean[0][~hit])
 
 
+@pytest.mark.parametrize("T,H,E", [(33, 128, 5), (500, 1152, 70), (600, 384, 33), (2000, 640, 256), (4604, 128, 257),
+                                   (700, 2048, 1000)])
+def test_router_backward_checkpoint_is_its_values(moe, T, H, E):
+    """From a checkpoint and from the bf16 values it restores: the same bits."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    codes, scales = moe.moe_ckpt_pack(torch.randn(T, H, generator=g, device="cuda").bfloat16())
+    dl, w = torch.randn(T, E, generator=g, device="cuda"), torch.randn(E, H, generator=g, device="cuda")
+    a = moe.moe_router_logits_backward(dl, w, codes=codes, scales=scales)
+    b = moe.moe_router_logits_backward(dl, w, x=moe.moe_ckpt_unpack(codes, scales))
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
 def test_router_backward_no_tokens(moe):
     E, H = 9, 128
     dl = torch.empty((0, E), device="cuda")
@@ -474,7 +487,8 @@ def wgrad_bound(dy, x):
     return (len(dy) + 8) * 2 * U * (np.abs(dy).T @ np.abs(x))
 
 
-@pytest.mark.parametrize("R,N,K", [(1, 8, 128), (1, 256, 256), (2, 136, 128), (7, 64, 384), (31, 264, 128), (64, 128, 512),
+@pytest.mark.parametrize("R,N,K", [(1, 8, 128), (1, 256, 256), (2, 136, 128), (7, 64, 384),
+                                   (31, 264, 128), (64, 128, 512),
                                    (65, 512, 256), (127, 1024, 128), (200, 248, 640), (513, 256, 256), (1000, 72, 896),
                                    (4604, 128, 128), (5000, 512, 1024), (0, 64, 128)])
 def test_wgrad_dense(moe, R, N, K):
@@ -519,6 +533,32 @@ def test_wgrad_by_expert(moe, T, k, G, N, K, via):
     acc = moe.moe_ckpt_wgrad(dyb, codes, scales, offsets=offsets, dw=base, accumulate=True, ws=ws, **kw)
     empty = np.flatnonzero(off[1:] == off[:-1])
     assert (host(acc)[empty] == 1).all() and (got[empty] == 0).all()
+
+
+@pytest.mark.parametrize("R,N,K,G,seed", [
+    (1, 8, 128, 1, 0), (40, 520, 640, 1, 1), (63, 256, 128, 3, 2), (128, 1032, 384, 1, 3), (129, 264, 256, 1, 4),
+    (200, 64, 512, 40, 5), (500, 776, 256, 4, 6), (900, 328, 1152, 16, 7), (2000, 136, 128, 16, 8), (5, 512, 512, 9, 9),
+])
+def test_wgrad_through_the_identity_table(moe, R, N, K, G, seed):
+    """With perm = 0, 1, .. a call takes the checkpoint's values from the
+    workspace, without it it may convert the codes in the product: the same bits,
+    for groups of any sizes, empty ones and rows in front and behind included."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    codes, scales = moe.moe_ckpt_pack(torch.randn(R, K, generator=g, device="cuda").bfloat16())
+    dy = torch.randn(R, N, generator=g, device="cuda").bfloat16()
+    cut = torch.randint(0, R + 1, (G + 1,), generator=g, device="cuda").sort()[0]
+    dy[int(cut[-1]):] = float("nan")
+    dy[: int(cut[0])] = float("inf")
+    off, perm = cut.int(), torch.arange(R, dtype=torch.int32, device="cuda")
+    ws = torch.full((moe.moe_ckpt_wgrad_workspace_bytes(R, N, K, G),), 0xFF, dtype=torch.uint8, device="cuda")
+    a = moe.moe_ckpt_wgrad(dy, codes, scales, offsets=off, ws=ws)
+    assert moe.moe_check_device_flag(ws) == 0
+    b = moe.moe_ckpt_wgrad(dy, codes, scales, offsets=off, perm=perm)
+    assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+    base = torch.randn(a.shape, generator=g, device="cuda")
+    c = moe.moe_ckpt_wgrad(dy, codes, scales, offsets=off, dw=base.clone(), accumulate=True)
+    assert torch.equal(c, base + a)
 
 
 def test_wgrad_groups_do_not_touch(moe):

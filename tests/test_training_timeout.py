@@ -20,7 +20,8 @@ def moe():
     return m
 
 
-@pytest.mark.parametrize("R,groups", [(40, None), (1000, None), (1000, [0, 333, 333, 1000])])
+@pytest.mark.parametrize("R,groups", [(40, None), (1000, None), (1000, [0, 333, 333, 1000]), (90, [0, 10, 10, 85]),
+                                      (600, None)])
 def test_withheld_stage_times_out_then_next_call_is_exact(moe, R, groups):
     g = torch.Generator(device="cuda")
     g.manual_seed(R)
