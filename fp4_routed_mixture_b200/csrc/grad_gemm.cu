@@ -757,9 +757,9 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                     }
                 }
                 gg_commit(smem_u32(&sh.drain));
+                // every MMA is done before either CTA frees its TMEM
+                final_wait(smem_u32(&sh.drain), 0);
             }
-            // every MMA is done before either CTA frees its TMEM
-            final_wait(smem_u32(&sh.drain), 0);
         } else if (Cfg::WGRAD && warp == 2 && FIRST) {
             if (blockIdx.x == 0) {
                 if (lane == 0) *a.flag = 0;
@@ -983,6 +983,10 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
+    // The last of the leader's arrivals here has landed before this CTA may end.
+    // (Its limit counts from the end of this CTA's own work: a wait from the start
+    // would bound the whole kernel instead of one hand-over.)
+    if (rank != 0 && threadIdx.x == 0) final_wait(smem_u32(&sh.drain), 0);
     gg_cluster_sync();      // no remote arrive or MMA targets this CTA any more
     if (threadIdx.x == 0 && *abort) {
         // (not before CTA 0 has cleared the word: it starts first, and 10 ms is long)

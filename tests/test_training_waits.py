@@ -1,0 +1,51 @@
+"""The gradient GEMM's bounded waits in calls that take longer than the limit.
+
+MOE_OPT_WAIT_LIMIT_US bounds one hand-over between the kernel's roles (a stage,
+an accumulator: microseconds), not a call, however long it runs: a healthy call
+raises nothing and stores everything.  No wait is made to run out here.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import fp4_routed_mixture_b200 as m
+    return m
+
+
+@pytest.fixture
+def limit(moe):
+    old = moe.moe_get_option(moe.MOE_OPT_WAIT_LIMIT_US)
+    yield lambda us: moe.moe_set_option(moe.MOE_OPT_WAIT_LIMIT_US, us)
+    moe.moe_set_option(moe.MOE_OPT_WAIT_LIMIT_US, old)
+
+
+def signs(shape, g):
+    """-1 and 1 as E4M3 codes, all scales 1."""
+    c = torch.randint(0, 2, shape, generator=g, device="cuda", dtype=torch.uint8).mul_(0x80).add_(0x38)
+    return c, torch.full((shape[0], shape[1] // 128), 127, dtype=torch.uint8, device="cuda")
+
+
+def test_call_longer_than_the_limit(moe, limit):
+    """2.1e14 operations: 0.13 s at the highest rate measured, and waits for what
+    is in flight last 0.1 s at the least.  Sums of at most 2^18 ones: exact."""
+    R, N, K = 1 << 18, 16384, 24576
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    codes, scales = signs((R, K), g)
+    dy = torch.randint(-1, 2, (R, N), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    ws = torch.empty(moe.moe_ckpt_wgrad_workspace_bytes(R, N, K), dtype=torch.uint8, device="cuda")
+    dw = torch.full((N, K), float("nan"), device="cuda")
+    limit(50000)
+    moe.moe_ckpt_wgrad(dy, codes, scales, dw=dw, ws=ws)
+    assert moe.moe_check_device_flag(ws) == 0
+    rows = torch.arange(5, N, 64, device="cuda")          # of every half tile
+    want = torch.zeros((len(rows), K), device="cuda")
+    for i in range(0, R, 8192):
+        want += dy[i:i + 8192][:, rows].float().t() @ (1.0 - 2.0 * (codes[i:i + 8192] >> 7).float())
+    assert torch.equal(dw[rows], want)
