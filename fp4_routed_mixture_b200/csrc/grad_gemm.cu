@@ -124,6 +124,7 @@ struct GradShared {
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int32_t abort;
+    uint32_t issued;         // stages whose copies this CTA has issued (modulo 2^32)
     int32_t rem_pre[GG_MAX_PAIRS + 1];               // chunks in front of each split tile
     float bias[4][32];
     uint8_t slots[MODE == GM_RDX ? 4 : 1][GG_MAX_PAIRS];
@@ -536,6 +537,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         }
         mbar_init(smem_u32(&sh.drain), 1);
         sh.abort = 0;
+        sh.issued = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1 && lane < 4) {
@@ -591,6 +593,17 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     // of a whole warp: its lanes go on or give up together
     auto warp_wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, !*abort && wait(bar, parity)) != 0;
+    };
+    // For a stage that may lie far ahead: the limit starts again as long as the
+    // stages in front of it are being issued (one writer, read here after a whole
+    // limit without success).
+    volatile uint32_t* issued = &sh.issued;
+    auto warp_wait_ahead = [&](uint32_t bar, uint32_t parity) {
+        for (;;) {
+            const uint32_t before = *issued;
+            if (warp_wait(bar, parity)) return true;
+            if (__any_sync(0xffffffffu, *abort || *issued == before)) return false;
+        }
     };
     // The waits for what is in flight are not cut short: 0.1 s at the least.
     const uint64_t drain_ns = max(a.wait_ns, (uint64_t)100000000);
@@ -685,6 +698,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                         gg_tma(dst + GG_BLOCK, &b_map, n + 64, r, p, bar);
                     }
                 }
+                if (Cfg::WGRAD && !CODES) *issued = *issued + 1;
                 next_stage();
             }
             // (a barrier's last use has the other parity than its next; one never used
@@ -874,7 +888,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             const int t = threadIdx.x - 32 * GG_TAIL_WARP0;
             for (Steps s(walk0); s.on; s.advance()) {
                 if (has_tail(s.seg, s.st)) {
-                    if (!warp_wait(smem_u32(&sh.tail_landed[stage]), next_parity(tails))) {
+                    if (!warp_wait_ahead(smem_u32(&sh.tail_landed[stage]), next_parity(tails))) {
                         give_up();
                         break;
                     }

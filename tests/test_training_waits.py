@@ -49,3 +49,24 @@ def test_call_longer_than_the_limit(moe, limit):
     for i in range(0, R, 8192):
         want += dy[i:i + 8192][:, rows].float().t() @ (1.0 - 2.0 * (codes[i:i + 8192] >> 7).float())
     assert torch.equal(dw[rows], want)
+
+
+def test_stage_with_a_tail_far_behind_the_first(moe, limit):
+    """A first group of whole stages, 0.15 ms of work, in front of a group that ends
+    inside a stage with rows behind it: the warps that clear those rows wait for
+    longer than the limit, for a stage that is on its way."""
+    R, N, K, cut = 16384, 4096, 4096, 8192
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    codes, scales = signs((R, K), g)
+    dy = torch.randint(-1, 2, (R, N), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    last = R - 77
+    dy[last:] = float("nan")
+    off = torch.tensor([0, cut, last], dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_ckpt_wgrad_workspace_bytes(R, N, K, 2), dtype=torch.uint8, device="cuda")
+    x = 1.0 - 2.0 * (codes >> 7).float()
+    want = torch.stack([dy[a:b].float().t() @ x[a:b] for a, b in ((0, cut), (cut, last))])
+    limit(100)
+    dw = moe.moe_ckpt_wgrad(dy, codes, scales, offsets=off, ws=ws)
+    assert moe.moe_check_device_flag(ws) == 0
+    assert torch.equal(dw, want)
