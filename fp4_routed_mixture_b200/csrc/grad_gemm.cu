@@ -85,9 +85,10 @@ static_assert(2 * GG_REGS_LOAD + 2 * GG_REGS_EPI <= 4 * GG_REGS, "registers of t
 // 512 27.2 / 26.3; 16 groups of 100 rows 222 / 219, of 400 326 / 268, of 800 486 / 467.
 constexpr int kFewRows = 256;
 // Up to this many rows a group, without perm, the kernel reads the codes itself
-// (us, GM_WGRAD_CODES / in front; 4096 x 4096: 40 rows 17.6 / 17.6, 128 19.1 / 18.9, 192
-// 21.7 / 19.9; 16 groups of 60 rows on average 190 / 213, of 100 198 / 221, of 128 217 / 222;
-// 64 rows, 16384 x 4096: 49 / 56; and one launch).
+// (us, GM_WGRAD_CODES / in front; one group: 512 x 512, 40 rows 8.5 / 8.0; 4096 x 4096, 1
+// row 19.9 / 18.5, 40 rows 20.0 / 19.5, 128 21.6 / 20.6; 16384 x 4096, 64 rows 52 / 57, 128
+// 58 / 60; 16 groups: 2048 x 2048, 40 rows 54 / 59, 4096 x 4096, 16 rows 179 / 201, 64 205 /
+// 216, 128 231 / 216; 128 groups of 1024 x 1024, 128 rows 120 / 135).
 constexpr int kConvertRows = 128;
 static_assert(kConvertRows <= kFewRows, "the form that converts");
 
@@ -630,8 +631,6 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
         return Cfg::WGRAD && s.r1 < a.R && s.r1 - s.r0 - st * GG_K < GG_K;
     };
     constexpr bool CODES = Cfg::CODES;
-    // No kernel in front has cleared the error word and checked the offsets.
-    constexpr bool FIRST = MODE == GM_WGRAD_CODES;
     auto next_parity = [&](uint32_t& bits) {
         const uint32_t p = bits >> stage & 1u;
         bits ^= 1u << stage;
@@ -773,12 +772,6 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                 gg_commit(smem_u32(&sh.drain));
                 // every MMA is done before either CTA frees its TMEM
                 final_wait(smem_u32(&sh.drain), 0);
-            }
-        } else if (Cfg::WGRAD && warp == 2 && FIRST) {
-            if (blockIdx.x == 0) {
-                if (lane == 0) *a.flag = 0;
-                __syncwarp();
-                if (a.offsets && bad_offsets(a.offsets, a.G, a.R, lane, 32)) raise_flag(a.flag, FLAG_BOUNDS);
             }
         } else if (Cfg::WGRAD && warp == 2 && a.perm) {
             // (k_grad_prepare reads row 0 for a bad entry; the error word is this
@@ -1002,12 +995,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     // would bound the whole kernel instead of one hand-over.)
     if (rank != 0 && threadIdx.x == 0) final_wait(smem_u32(&sh.drain), 0);
     gg_cluster_sync();      // no remote arrive or MMA targets this CTA any more
-    if (threadIdx.x == 0 && *abort) {
-        // (not before CTA 0 has cleared the word: it starts first, and 10 ms is long)
-        const uint64_t t0 = global_ns();
-        while (FIRST && global_ns() - t0 < 10000000) __nanosleep(10000);
-        raise_flag(a.flag, FLAG_TIMEOUT);
-    }
+    if (threadIdx.x == 0 && *abort) raise_flag(a.flag, FLAG_TIMEOUT);
     tc_fence_after();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
@@ -1343,24 +1331,25 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
     cudaError_t e = cudaSuccess;
     __nv_bfloat16* xb = (__nv_bfloat16*)((char*)ws + 256);
     const bool convert = R > 0 && !perm && R / G <= kConvertRows;
-    if (!convert) {
-        PrepareArgs s = {};
-        s.codes = codes;
-        s.scales = scales;
-        s.items = (long long)R * (K / 8);
-        s.K = K;
-        s.perm = perm;
-        s.k_div = k;
-        s.xrows = rows;
-        s.xb = xb;
-        s.offsets = offsets;
-        s.G = G;
-        s.R = R;
-        s.flag = flag;
-        e = launch_pdl(k_grad_prepare, dim3(std::max(1u, prepare_ctas(s.items))), dim3(kSplitThreads), 0, st, s);
-        count_launches(1);
-        if (e == cudaSuccess && R == 0) return accumulate ? e : cudaMemsetAsync(dw, 0, sizeof(float) * G * N * K, st);
-    }
+    // (the form that converts has one CTA here, for the error word and the offsets: a
+    // clear inside the product's grid would not be ordered before another CTA's flag.
+    // It costs 2 us: 512 x 512 6.9 -> 8.5, 4096 x 4096 17.9 -> 19.9)
+    PrepareArgs s = {};
+    s.codes = codes;
+    s.scales = scales;
+    s.items = convert ? 0 : (long long)R * (K / 8);
+    s.K = K;
+    s.perm = perm;
+    s.k_div = k;
+    s.xrows = rows;
+    s.xb = xb;
+    s.offsets = offsets;
+    s.G = G;
+    s.R = R;
+    s.flag = flag;
+    e = launch_pdl(k_grad_prepare, dim3(std::max(1u, prepare_ctas(s.items))), dim3(kSplitThreads), 0, st, s);
+    count_launches(1);
+    if (e == cudaSuccess && R == 0) return accumulate ? e : cudaMemsetAsync(dw, 0, sizeof(float) * G * N * K, st);
     CUtensorMap a_map, b_map;
     if (e == cudaSuccess) e = bf16_map(dy, lddy, R, N, 1, GG_K, &a_map);
     if (e == cudaSuccess)

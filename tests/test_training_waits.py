@@ -2,7 +2,7 @@
 
 MOE_OPT_WAIT_LIMIT_US bounds one hand-over between the kernel's roles (a stage,
 an accumulator: microseconds), not a call, however long it runs: a healthy call
-raises nothing and stores everything.  No wait is made to run out here.
+raises nothing and stores everything.
 """
 import pytest
 import torch
@@ -70,3 +70,31 @@ def test_stage_with_a_tail_far_behind_the_first(moe, limit):
     dw = moe.moe_ckpt_wgrad(dy, codes, scales, offsets=off, ws=ws)
     assert moe.moe_check_device_flag(ws) == 0
     assert torch.equal(dw, want)
+
+
+@pytest.mark.parametrize("groups", [None, [0, 10, 10, 33]])
+def test_error_word_is_cleared_in_front_of_the_product(moe, limit, groups):
+    """Few rows, where the product reads the codes itself: the word is cleared by a
+    launch in front (a clear by one block of the product's own grid may come after
+    another block's flag and take it away), and a flag raised at once stays."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    codes, scales = signs((40, 256), g)
+    dy = torch.randn(40, 512, generator=g, device="cuda").bfloat16()
+    off = None if groups is None else torch.tensor(groups, dtype=torch.int32, device="cuda")
+    G = 1 if groups is None else len(groups) - 1
+    ws = torch.full((moe.moe_ckpt_wgrad_workspace_bytes(40, 512, 256, G),), 0xA5, dtype=torch.uint8, device="cuda")
+    before = moe.moe_launch_count()
+    want = moe.moe_ckpt_wgrad(dy, codes, scales, offsets=off, ws=ws)
+    assert moe.moe_launch_count() - before == 2
+    assert moe.moe_check_device_flag(ws) == 0
+    limit(1)
+    moe.moe_set_option(moe.MOE_OPT_TEST_GRAD_TIMEOUT, 1)
+    try:
+        moe.moe_ckpt_wgrad(dy, codes, scales, offsets=off, ws=ws)
+        assert moe.moe_check_device_flag(ws) == moe.FLAG_TIMEOUT
+    finally:
+        moe.moe_set_option(moe.MOE_OPT_TEST_GRAD_TIMEOUT, 0)
+    limit(1000000)
+    assert torch.equal(moe.moe_ckpt_wgrad(dy, codes, scales, offsets=off, ws=ws), want)
+    assert moe.moe_check_device_flag(ws) == 0
