@@ -401,6 +401,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(RouteBackwardA
     if (first >= a.T) return;
     const int r0 = (int)first, r1 = (int)min((long long)a.T, first + a.rows);
     int s = -1, s_end = r0;       // the sequence whose f is in registers ends at s_end
+    bool has = false;             // that sequence has rows
     float f[N], w = 0.0f;
     float nx[N], ng = 0.0f, ndg = 0.0f;
     int nid = -1, non = 1;
@@ -431,8 +432,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(RouteBackwardA
             const bool in = s < a.seq.S && a.seq.at(s) <= r;
             const int n = in ? __ldg(a.tokens + s) : 0;
             const int used = __ldg(a.tokens + a.seq.S);
-            w = 0.0f;
-            if (n > 0 && used > 0) {
+            has = n > 0 && used > 0;
+            if (has) {
                 const float inv = 1.0f / (float)n;
                 w = __ldg(a.dloss) * (a.coef / (float)used) * inv;
                 const float fs = (float)a.E / (float)a.k * inv;
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(RouteBackwardA
                 if (!in) s_end = min(s_end, r + 1);
             }
         }
-        if (on && w != 0.0f) {
+        if (on && has) {         // (a weight w of 0 too: it times a NaN is NaN)
             float sum = row_exp<N>(x), dot = 0.0f;
 #pragma unroll
             for (int v = 0; v < N; ++v) dot = fmaf(x[v], f[v], dot);

@@ -1,0 +1,45 @@
+"""The training operators at the edges of their documentation."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import fp4_routed_mixture_b200 as m
+    return m
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def routed(moe, T, E, k, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    z = torch.randn(T, E, generator=g, device="cuda")
+    return z, *moe.moe_route(z, k)
+
+
+@pytest.mark.parametrize("E", [8, 7, 256, 300])
+@pytest.mark.parametrize("coef,dloss", [(1.0, 1.0), (0.0, 1.0), (1.0, 0.0)])
+def test_route_backward_keeps_nan_at_weight_zero(moe, E, coef, dloss):
+    """The balance term is weight * p * (f - p f): NaN in a row whose softmax is,
+    whatever the weight; 0 in the others at weight 0; masked rows are out of it."""
+    z, idx, _ = routed(moe, 9, E, 2, E)
+    z[2, 3] = float("nan")
+    z[4, 1] = float("inf")
+    z[6, 0] = float("nan")
+    mask = torch.ones(9, dtype=torch.bool, device="cuda")
+    mask[6] = False
+    _, counts, _, tokens = moe.moe_balance_loss(z, idx, 1.0, seq_offsets=i32(0, 4, 8), token_mask=mask)
+    d = moe.moe_route_backward(z, idx, dloss=torch.full((1,), dloss, device="cuda"), coef=coef, counts=counts,
+                               tokens=tokens, seq_offsets=i32(0, 4, 8), token_mask=mask)
+    nan = torch.isnan(d)
+    assert nan.all(1).tolist() == nan.any(1).tolist() == [t in (2, 4) for t in range(9)]
+    rest = [0, 1, 3, 5, 7]
+    assert bool((d[rest] != 0).any(1).all()) == (coef * dloss != 0)
+    assert not d[[6, 8]].any()                  # masked; behind the last sequence
