@@ -351,20 +351,24 @@ __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(BalanceArgs a) {
     }
 }
 
-// No tokens: every output is zero.
-__global__ void k_balance_empty(int32_t* head, int32_t* counts, float* mean_prob, int32_t* tokens, float* loss,
-                                int E, int S) {
+// No tokens: every output is zero.  (The first CTA checks the offsets.)
+__global__ void k_balance_empty(SeqTable seq, int32_t* head, int32_t* counts, float* mean_prob, int32_t* tokens,
+                                float* loss, int E) {
     pdl_begin();
+    const int S = seq.S;
+    if (blockIdx.x == 0) {
+        bool bad = false;
+        for (int s = threadIdx.x; s < S; s += blockDim.x) bad |= seq.bad(s);
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *head = bad ? FLAG_BOUNDS : 0;
+    }
     const size_t n = (size_t)S * E, i0 = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
     for (size_t i = i0; i < n; i += (size_t)gridDim.x * blockDim.x) {
         counts[i] = 0;
         if (mean_prob) mean_prob[i] = 0.0f;
     }
     for (size_t i = i0; i <= (size_t)S; i += (size_t)gridDim.x * blockDim.x) tokens[i] = 0;
-    if (i0 == 0) {
-        *head = 0;
-        *loss = 0.0f;
-    }
+    if (i0 == 0) *loss = 0.0f;
 }
 
 // ---- gradient of the logits ----------------------------------------------------
@@ -553,7 +557,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const i
     cudaError_t e;
     if (T == 0) {
         e = launch_pdl(k_balance_empty, dim3((unsigned)std::min<size_t>(((size_t)S * E + 255) / 256 + 1, 592)), dim3(256), 0, st,
-                       head, counts, mean_prob, tokens, loss, E, S);
+                       SeqTable{seq_off, T, S}, head, counts, mean_prob, tokens, loss, E);
         count_launches(1);
         return e;
     }

@@ -43,3 +43,14 @@ def test_route_backward_keeps_nan_at_weight_zero(moe, E, coef, dloss):
     rest = [0, 1, 3, 5, 7]
     assert bool((d[rest] != 0).any(1).all()) == (coef * dloss != 0)
     assert not d[[6, 8]].any()                  # masked; behind the last sequence
+
+
+@pytest.mark.parametrize("seq,bad", [((0, 0, 0), 0), ((0, 5, 0), 1), ((0, 0, 3), 1), ((-1, 0, 0), 1),
+                                     ((0,) * 700 + (2,), 1), ((0,) * 701, 0)])
+def test_balance_of_no_tokens_checks_the_offsets(moe, seq, bad):
+    S, E = len(seq) - 1, 8
+    ws = torch.full((moe.moe_balance_workspace_bytes(0, E, S),), 0xA5, dtype=torch.uint8, device="cuda")
+    z, idx = torch.empty((0, E), device="cuda"), torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    loss, counts, prob, tokens = moe.moe_balance_loss(z, idx, 1.0, seq_offsets=i32(*seq), ws=ws)
+    assert moe.moe_check_device_flag(ws) == (moe.FLAG_BOUNDS if bad else 0)
+    assert not loss.any() and not counts.any() and not prob.any() and not tokens.any()
