@@ -295,6 +295,8 @@ __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(BalanceArgs a) {
     sp[warp][lane] = p;
     sc[warp][lane] = h;
     if (lane == 0) sn[warp] = n;
+    // (with offsets that do not ascend a slot may be one that no chunk has written)
+    bad &= FLAG_BAD_EXPERT;
     if (bad && lane == 0 && cb == 0) raise_flag(a.head, bad);
     __syncthreads();
     if (warp == 0) {

@@ -340,7 +340,8 @@ int moe_fp8_linear(const void *x_bf16, int T, int N, int K, const void *packed, 
  * ws: moe_balance_workspace_bytes(T_max, E, S_max) bytes, 256-byte aligned,
  * T <= T_max, S <= S_max; its first int32 is the device error word, cleared by
  * this call: MOE_FLAG_BAD_EXPERT for an id outside [0, E) (left out of the
- * counts), MOE_FLAG_BOUNDS for offsets that do not ascend within [0, T].
+ * counts), MOE_FLAG_BOUNDS for offsets that do not ascend within [0, T] (what
+ * the outputs hold is then unspecified, and MOE_FLAG_BAD_EXPERT may be set too).
  * 1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 65535. */
 size_t moe_balance_workspace_bytes(int T_max, int E, int S_max);
 int moe_balance_loss(const float *logits, const int32_t *topk_idx, const int32_t *seq_offsets,

@@ -54,3 +54,20 @@ def test_balance_of_no_tokens_checks_the_offsets(moe, seq, bad):
     loss, counts, prob, tokens = moe.moe_balance_loss(z, idx, 1.0, seq_offsets=i32(*seq), ws=ws)
     assert moe.moe_check_device_flag(ws) == (moe.FLAG_BOUNDS if bad else 0)
     assert not loss.any() and not counts.any() and not prob.any() and not tokens.any()
+
+
+@pytest.mark.parametrize("seq", [(0, 700, 300, 1000), (0, 900, 100, 200, 1000), (400, 0, 1000), (0, 500, 1001)])
+def test_balance_bad_offsets_in_a_used_workspace(moe, seq):
+    """Many rows, where offsets that do not ascend make the sum read places of the
+    workspace that the call has not written: no bits but the documented ones."""
+    T, E = 1000, 16
+    z, idx, _ = routed(moe, T, E, 2, 3)
+    n = moe.moe_balance_workspace_bytes(T, E, len(seq) - 1)
+    for fill in (0xA5, 0xFF, 0):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        moe.moe_balance_loss(z, idx, 1.0, seq_offsets=i32(*seq), ws=ws)
+        flag = moe.moe_check_device_flag(ws)
+        assert flag & moe.FLAG_BOUNDS and not flag & ~(moe.FLAG_BOUNDS | moe.FLAG_BAD_EXPERT)
+    a = moe.moe_balance_loss(z, idx, 1.0, ws=ws)
+    assert moe.moe_check_device_flag(ws) == 0
+    assert all(torch.equal(u, v) for u, v in zip(a, moe.moe_balance_loss(z, idx, 1.0)))
