@@ -6,6 +6,7 @@
 #include <cstddef>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 
 #include "../../include/moe.h"
@@ -644,8 +645,24 @@ int moe_fp8_linear(const void* x_bf16, int T, int N, int K, const void* packed, 
 // Rows and columns whose products and sums the kernels hold in 32 bits.
 constexpr int kTrainMaxRows = 1 << 30, kTrainMaxCols = 1 << 20;
 
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    return a && b && na && nb && (const char*)a < (const char*)b + nb && (const char*)b < (const char*)a + na;
+// Memory a call reads or writes (p NULL or n 0: none).
+struct Span {
+    const void* p;
+    size_t n;
+};
+static bool overlap(const Span& a, const Span& b) {
+    return a.p && b.p && a.n && b.n && (const char*)a.p < (const char*)b.p + b.n && (const char*)b.p < (const char*)a.p + a.n;
+}
+// Other blocks may still have to read what an output that lies on it overwrites.
+static int check_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins, const char* who) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& i : ins)
+            if (overlap(*o, i)) return fail(MOE_ERR_INVALID_ARG, "%s: an output or the workspace overlaps an input", who);
+        for (auto p = o + 1; p != outs.end(); ++p)
+            if (overlap(*o, *p))
+                return fail(MOE_ERR_INVALID_ARG, "%s: an output overlaps another one or the workspace", who);
+    }
+    return MOE_OK;
 }
 // Bytes from the first to the last of T rows of `cols` bf16, ld apart.
 static size_t span_bf16(int T, int cols, int64_t ld) { return T > 0 ? 2 * ((size_t)(T - 1) * ld + cols) : 0; }
@@ -684,6 +701,12 @@ int moe_balance_loss(const float* logits, const int32_t* topk_idx, const int32_t
     if (ws_bytes < moe::balance_workspace_bytes(T, E, S))
         return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: ws_bytes %zu < %zu", ws_bytes,
                     moe::balance_workspace_bytes(T, E, S));
+    const size_t rows = T, offs = 4 * ((size_t)S + 1), table = 4 * (size_t)S * E;
+    if (int rc = check_overlap({{counts, table}, {mean_prob, table}, {tokens, offs}, {loss, 4},
+                                {ws, moe::balance_workspace_bytes(T, E, S)}},
+                               {{logits, 4 * rows * E}, {topk_idx, 4 * rows * k}, {seq_offsets, offs}, {token_mask, rows}},
+                               "moe_balance_loss"))
+        return rc;
     cudaError_t e = moe::launch_balance_loss(logits, topk_idx, seq_offsets, token_mask, T, E, k, S, coef, counts,
                                              mean_prob, tokens, loss, ws, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_balance_loss launch");
@@ -703,9 +726,14 @@ int moe_route_backward(const float* logits, const int32_t* topk_idx, const float
         !aligned(dloss, 4) || !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(seq_offsets, 4) ||
         !aligned(dlogits, 4) || !aligned(flag, 4))
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: the tensors need 4-byte alignment");
-    const size_t bytes = 4 * (size_t)T * E;
-    if (overlap(dlogits, bytes, logits, bytes))
-        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: dlogits overlaps logits");
+    // (what a NULL dloss or dgates leaves unread may lie anywhere)
+    const size_t rows = T, offs = dloss ? 4 * ((size_t)S + 1) : 0, gn = dgates ? 4 * rows * k : 0;
+    if (int rc = check_overlap({{dlogits, 4 * rows * E}, {flag, 4}},
+                               {{logits, 4 * rows * E}, {topk_idx, gn}, {gates, gn}, {dgates, gn}, {dloss, 4},
+                                {counts, dloss ? 4 * (size_t)S * E : 0}, {tokens, offs}, {seq_offsets, offs},
+                                {token_mask, dloss ? rows : 0}},
+                               "moe_route_backward"))
+        return rc;
     cudaError_t e = moe::launch_route_backward(logits, topk_idx, gates, dgates, dloss, counts, tokens, seq_offsets,
                                                token_mask, T, E, k, S, coef, dlogits, flag, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_route_backward launch");
@@ -742,13 +770,13 @@ int moe_router_logits_backward(const float* dlogits, const void* x_bf16, const u
     if (ws_bytes < moe::router_backward_workspace_bytes(T, H, E))
         return fail(MOE_ERR_INVALID_ARG, "%s: ws_bytes %zu < %zu", who, ws_bytes,
                     moe::router_backward_workspace_bytes(T, H, E));
-    const size_t dl_n = 4 * (size_t)T * E, w_n = 4 * (size_t)E * H, x_n = (size_t)T * H;
-    if (overlap(dx_bf16, 2 * x_n, dlogits, dl_n) || overlap(dx_bf16, 2 * x_n, x_bf16, 2 * x_n) ||
-        overlap(dx_bf16, 2 * x_n, x_codes, x_n) || overlap(dx_bf16, 2 * x_n, w_router, w_n) ||
-        overlap(dw, w_n, dlogits, dl_n) || overlap(dw, w_n, x_bf16, 2 * x_n) || overlap(dw, w_n, x_codes, x_n) ||
-        overlap(dw, w_n, w_router, w_n) || overlap(dx_bf16, 2 * x_n, dw, w_n) ||
-        overlap(dbias, 4 * (size_t)E, dlogits, dl_n))
-        return fail(MOE_ERR_INVALID_ARG, "%s: an output overlaps an input or the other output", who);
+    const size_t rows = T, w_n = 4 * (size_t)E * H, x_n = rows * H;
+    if (int rc = check_overlap({{dx_bf16, 2 * x_n}, {dw, w_n}, {dbias, 4 * (size_t)E},
+                                {ws, moe::router_backward_workspace_bytes(T, H, E)}},
+                               {{dlogits, 4 * rows * E}, {x_bf16, 2 * x_n}, {x_codes, x_n}, {x_scales, x_n / 128},
+                                {w_router, w_n}},
+                               who))
+        return rc;
     cudaError_t e = moe::launch_router_backward(dlogits, x_bf16, x_codes, x_scales, w_router, T, H, E, dx_bf16, dw,
                                                 dbias, accumulate, ws, load_options().wait_ns, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, who);
@@ -776,8 +804,7 @@ int moe_ckpt_pack(const void* x_bf16, int64_t ldx, int T, int K, uint8_t* codes,
     if (!aligned(x_bf16, 16) || !aligned(codes, 16))
         return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_pack: x and codes need 16-byte alignment");
     const size_t n = (size_t)T * K, xn = span_bf16(T, K, ldx);
-    if (overlap(codes, n, x_bf16, xn) || overlap(scales, n / 128, x_bf16, xn))
-        return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_pack: the checkpoint overlaps x");
+    if (int rc = check_overlap({{codes, n}, {scales, n / 128}}, {{x_bf16, xn}}, "moe_ckpt_pack")) return rc;
     cudaError_t e = moe::launch_ckpt_pack(x_bf16, ldx, T, K, codes, scales, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_ckpt_pack launch");
 }
@@ -791,8 +818,7 @@ int moe_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, int T, int K, v
     if (!aligned(x_bf16, 16) || !aligned(codes, 16))
         return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_unpack: x and codes need 16-byte alignment");
     const size_t n = (size_t)T * K, xn = span_bf16(T, K, ldx);
-    if (overlap(codes, n, x_bf16, xn) || overlap(scales, n / 128, x_bf16, xn))
-        return fail(MOE_ERR_INVALID_ARG, "moe_ckpt_unpack: x overlaps the checkpoint");
+    if (int rc = check_overlap({{x_bf16, xn}}, {{codes, n}, {scales, n / 128}}, "moe_ckpt_unpack")) return rc;
     cudaError_t e = moe::launch_ckpt_unpack(codes, scales, T, K, x_bf16, ldx, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_ckpt_unpack launch");
 }
@@ -808,11 +834,9 @@ int moe_ckpt_swiglu_backward(const uint8_t* gu_codes, const uint8_t* gu_scales, 
     if (!aligned(gu_codes, 16) || !aligned(dh_bf16, 16) || !aligned(dgu_bf16, 16) || !aligned(h_bf16, 16))
         return fail(MOE_ERR_INVALID_ARG, "%s: codes, dh, dgu and h need 16-byte alignment", who);
     const size_t n = (size_t)T * I, dn = span_bf16(T, I, lddh);
-    if (overlap(dgu_bf16, 4 * n, gu_codes, 2 * n) || overlap(dgu_bf16, 4 * n, gu_scales, 2 * n / 128) ||
-        overlap(dgu_bf16, 4 * n, dh_bf16, dn) || overlap(dgu_bf16, 4 * n, h_bf16, 2 * n) ||
-        overlap(h_bf16, 2 * n, gu_codes, 2 * n) || overlap(h_bf16, 2 * n, gu_scales, 2 * n / 128) ||
-        overlap(h_bf16, 2 * n, dh_bf16, dn))
-        return fail(MOE_ERR_INVALID_ARG, "%s: an output overlaps an input or the other output", who);
+    if (int rc = check_overlap({{dgu_bf16, 4 * n}, {h_bf16, 2 * n}},
+                               {{gu_codes, 2 * n}, {gu_scales, 2 * n / 128}, {dh_bf16, dn}}, who))
+        return rc;
     cudaError_t e = moe::launch_ckpt_swiglu_backward(gu_codes, gu_scales, dh_bf16, lddh, T, I, dgu_bf16, h_bf16, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, who);
 }
@@ -852,9 +876,12 @@ int moe_ckpt_wgrad(const void* dy_bf16, int64_t lddy, const uint8_t* x_codes, co
     if (ws_bytes < moe::wgrad_workspace_bytes(R, N, K, G))
         return fail(MOE_ERR_INVALID_ARG, "%s: ws_bytes %zu < %zu", who, ws_bytes,
                     moe::wgrad_workspace_bytes(R, N, K, G));
-    const size_t wn = 4 * (size_t)G * N * K;
-    if (overlap(dw, wn, dy_bf16, span_bf16(R, N, lddy)) || overlap(dw, wn, x_codes, (size_t)X * K))
-        return fail(MOE_ERR_INVALID_ARG, "%s: dw overlaps an input", who);
+    const size_t xn = (size_t)X * K;
+    if (int rc = check_overlap({{dw, 4 * (size_t)G * N * K}, {ws, moe::wgrad_workspace_bytes(R, N, K, G)}},
+                               {{dy_bf16, span_bf16(R, N, lddy)}, {x_codes, xn}, {x_scales, xn / 128},
+                                {offsets, 4 * ((size_t)G + 1)}, {perm, 4 * (size_t)R}},
+                               who))
+        return rc;
     cudaError_t e = moe::launch_ckpt_wgrad(dy_bf16, lddy, x_codes, x_scales, offsets, perm, k_div, R, X, N, K, G, dw,
                                            accumulate, ws, load_options().wait_ns,
                                            R > 0 ? g_test_grad_timeout.exchange(0) : 0, stream);

@@ -315,10 +315,11 @@ int moe_fp8_linear(const void *x_bf16, int T, int N, int K, const void *packed, 
  * no training; these calls use the usual definitions and this library's own
  * routing (moe_route), sort (moe_sort) and FP8 block format (moe_fp8_linear).
  * All are asynchronous and graph-capturable, and their results do not depend
- * on the order in which thread blocks run.  They take at most 2^30 rows, and no
- * output may overlap an input or another output.  A workspace (and its error word)
- * belongs to one call at a time: calls and replayed graphs that may overlap
- * need one each.
+ * on the order in which thread blocks run.  They take at most 2^30 rows.  No
+ * output and no workspace (nor moe_route_backward's flag) may overlap an input,
+ * another output or the workspace: such a call returns MOE_ERR_INVALID_ARG.  A
+ * workspace (and its error word) belongs to one call at a time: calls and
+ * replayed graphs that may overlap need one each.
  * ------------------------------------------------------------------------- */
 
 /* Load-balance loss and per-expert counts of routed tokens.
