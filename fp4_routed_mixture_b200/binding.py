@@ -438,16 +438,27 @@ def _rows(t, name: str, dtype, shape, dev):
     return p, shape[1] if shape[0] < 2 or t.is_contiguous() else t.stride(0)
 
 
+def _i32(name: str, *values):
+    """Sizes pass as C ints, to which ctypes would cut a larger one silently."""
+    for v in values:
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise MoeError(-2, f"{name}: {v} is beyond 32 bits")
+
+
 def _matrix(t, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         _bad(f"{name} must be a 2-D CUDA tensor")
-    return t.shape
+    rows, cols = shape = t.shape
+    if rows > 0x7fffffff or cols > 0x7fffffff:
+        _i32(name, rows, cols)
+    return shape
 
 
 def _table(t, name: str) -> int:
     """Groups a table of offsets bounds (its length less one)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.numel() < 2:
         _bad(f"{name} must be a 1-D tensor of at least two entries")
+    _i32(name, t.numel())
     return t.numel() - 1
 
 
@@ -496,6 +507,7 @@ def _call(dev, fn, args, stream):
 
 
 def moe_balance_workspace_bytes(T_max: int, E: int, S_max: int = 1) -> int:
+    _i32("moe_balance_workspace_bytes", T_max, E, S_max)
     n = lib.moe_balance_workspace_bytes(T_max, E, S_max)
     if n == 0:
         raise MoeError(-2, "unsupported dims")
@@ -553,6 +565,7 @@ def moe_route_backward(logits, topk_idx, gates=None, dgates=None, dloss=None, co
 
 
 def moe_router_backward_workspace_bytes(T_max: int, H: int, E: int) -> int:
+    _i32("moe_router_backward_workspace_bytes", T_max, H, E)
     n = lib.moe_router_backward_workspace_bytes(T_max, H, E)
     if n == 0:
         raise MoeError(-2, "unsupported dims")
@@ -631,6 +644,7 @@ def moe_ckpt_swiglu_backward(gu_codes, gu_scales, dh, need_h: bool = False, out=
 
 
 def moe_ckpt_wgrad_workspace_bytes(R_max: int, N: int, K: int, G: int = 1) -> int:
+    _i32("moe_ckpt_wgrad_workspace_bytes", R_max, N, K, G)
     n = lib.moe_ckpt_wgrad_workspace_bytes(R_max, N, K, G)
     if n == 0:
         raise MoeError(-2, "unsupported dims")
@@ -646,6 +660,7 @@ def moe_ckpt_wgrad(dy, codes, scales, offsets=None, perm=None, k: int = 1, dw=No
     X, K = _matrix(codes, "codes")
     dev = dy.device
     G = 1 if offsets is None else _table(offsets, "offsets")
+    _i32("k", k)
     shape = (N, K) if offsets is None else (G, N, K)
     if dw is None:
         if accumulate:

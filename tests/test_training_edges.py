@@ -71,3 +71,22 @@ def test_balance_bad_offsets_in_a_used_workspace(moe, seq):
     a = moe.moe_balance_loss(z, idx, 1.0, ws=ws)
     assert moe.moe_check_device_flag(ws) == 0
     assert all(torch.equal(u, v) for u, v in zip(a, moe.moe_balance_loss(z, idx, 1.0)))
+
+
+def test_sizes_beyond_32_bits_are_refused(moe):
+    """2^32 + 8 rows and k = 2^32 + 1 would arrive in C as 8 and 1."""
+    T = (1 << 32) + 8
+    z, idx = torch.zeros((T, 1), device="cuda"), torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_balance_workspace_bytes(8, 1, 1), dtype=torch.uint8, device="cuda")
+    out = (torch.empty(1, device="cuda"), i32(0).view(1, 1), None, i32(0, 0))
+    before = moe.moe_launch_count()
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_balance_loss(z, idx, 1.0, ws=ws, out=out)
+    assert e.value.status == -2
+    del z, idx
+    codes, scales = moe.moe_ckpt_pack(torch.zeros((16, 128), dtype=torch.bfloat16, device="cuda"))
+    dy = torch.zeros((16, 8), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_ckpt_wgrad(dy, codes, scales, perm=torch.arange(16, dtype=torch.int32, device="cuda"), k=(1 << 32) + 1)
+    assert e.value.status == -2
+    assert moe.moe_launch_count() == before + 1          # the pack alone
