@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
             const uint32_t bytes = (CODES ? AP : AP + BP) * GG_PLANE;
             constexpr uint32_t code_bytes = GG_K * GG_HALF;
             bool first = true;
+            uint32_t count = 0;
             for (Steps s(walk0); s.on; s.advance()) {
                 if (!gg_wait(smem_u32(&sh.empty[stage]), phase ^ 1u, drain_ns, nullptr)) {
                     give_up();
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
                         gg_tma(dst + GG_BLOCK, &b_map, n + 64, r, p, bar);
                     }
                 }
-                if (Cfg::WGRAD && !CODES) *issued = *issued + 1;
+                if (Cfg::WGRAD && !CODES) *issued = ++count;      // (no load: 8 percent of the call)
                 next_stage();
             }
             // (a barrier's last use has the other parity than its next; one never used
