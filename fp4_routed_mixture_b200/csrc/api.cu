@@ -785,7 +785,8 @@ int moe_router_logits_backward(const float* dlogits, const void* x_bf16, const u
 static int check_ckpt_dims(int T, int K, const char* who) {
     if (int rc = check_train_rows(T, who)) return rc;
     if (K <= 0 || K % 128 || K > (1 << 24))
-        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: the row length must be a positive multiple of 128 (got %d)", who, K);
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: the row length must be a positive multiple of 128, at most 2^24 (got %d)",
+                    who, K);
     return MOE_OK;
 }
 static int check_stride(int64_t ld, int cols, const char* who) {

@@ -24,12 +24,19 @@
 
 namespace moe {
 
-constexpr int kBalThreads = 512;             // k_balance_rows: 2 CTAs per SM
+// k_balance_rows: 2 CTAs per SM up to 256 experts (64 registers at most); above,
+// 106 to 125 registers leave room for one, and the chunks run in two waves.
+constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalMaxChunks = 148 * 2;
 constexpr int kRedThreads = 1024, kRedWarps = kRedThreads / 32;
-// Calls of at most this many rows and sequences run in one CTA and launch (8
-// rows of 256 logits: one launch of 3 us less).
+// Calls of at most this many rows and sequences run in one CTA and launch, which
+// walks the sequences one after the other (1.2 us each at 256 logits, 2.5 at 1024):
+// less time where they are few.  Measured (us, one launch / two; 256 logits): 8 rows, 1
+// sequence 2.9 / 7.6, 4 sequences 6.6 / 10.9; 32 rows, 4 7.1 / 8.8, 16 21.9 / 15.9; 128 rows,
+// 1 6.3 / 7.4, 4 9.7 / 7.6, 16 24 / 8.9, 64 83 / 23; 1024 logits, 128 rows, 1 11.3 / 9.1, 64
+// 163 / 59.  So above 4 to 8 sequences, and for 128 rows of 1024 logits, two launches
+// would take less: the bounds are higher than they should be.
 constexpr int kBalSingleT = 128, kBalSingleS = 64;
 
 struct BalanceWs {
@@ -396,7 +403,10 @@ struct RouteBackwardArgs {
 // gates' terms are added to the stored row in memory: comparing each of the k
 // ids with a lane's columns in registers took two thirds of the instructions.
 // 65536 x 256 logits: 25 us (134 MB, 5.4 TB/s), 28 us with 6 gates a row; the
-// terms through shared memory 7 us more, two or three rows loaded ahead 9.
+// terms through shared memory 7 us more, two or three rows loaded ahead 9.  What
+// bounds it besides HBM is the grid: rows a warp are set for 48 warps per SM, but
+// 64 registers let 32 run (E <= 256; 16 up to 512, 8 above), so that 16384 and 65536
+// rows, 1024 blocks for 592 places, take 1.73 waves.
 constexpr int kRouteThreads = 256, kRouteWarps = kRouteThreads / 32;
 
 template <int N, bool VEC>

@@ -17,8 +17,8 @@
 // 1500 cycles anyway, four warps convert the codes between their copy and the MMA
 // (GM_.._CODES): in dW of the router, three products a stage (16384 tokens, H 4096,
 // 256 experts, with dx: 217 us with the values in the workspace, 187 without), and
-// with few rows, where C's stores bound (16 groups of 20 rows on average, 4096 x 4096:
-// 202 us / 176).  In GM_WGRAD a stage's MMAs take 512 cycles: 750 us for 16384 x 4096 x
+// with few rows, where C's stores bound (16 groups of 16 rows, 4096 x 4096: 201 us /
+// 179).  In GM_WGRAD a stage's MMAs take 512 cycles: 750 us for 16384 x 4096 x
 // 4096, where the conversion in front costs 3 bytes of traffic per value and 30 us
 // of 465.
 //
@@ -47,10 +47,10 @@
 // and added up in the epilogue's registers, rounding to nearest.
 //
 // Bound by the tensor cores and, in long runs, the power limit.  Measured (one
-// B200): 16384 x 4096 x 4096 in 0.33-0.35 ms under ncu (1.6 PFLOP/s, tensor pipe
-// 86 percent busy; cuBLAS on bf16 operands 0.355 ms), whole call 0.40 ms in a
-// burst and 0.47 in a loop of seconds (cuBLAS there 0.39-0.415); 16 groups of
-// 1726 rows on average, 4096 x 4096: 0.70 ms (1.3 PFLOP/s), bound by the tensor
+// B200): 16384 x 4096 x 4096 in 0.34 ms under ncu (1.6 PFLOP/s, tensor pipe 86
+// percent busy; cuBLAS on bf16 operands 0.355 ms), whole call 0.40 ms in a burst and
+// 0.47 in a loop of seconds, 0.43 of it the GEMM (cuBLAS there 0.39-0.415); 16 groups
+// of 1726 rows on average, 4096 x 4096: 0.68 ms (1.36 PFLOP/s), bound by the tensor
 // cores beside 1.07 GB of results.
 #include "bf16_parts.cuh"
 #include "ckpt.cuh"
@@ -74,7 +74,8 @@ constexpr int GG_THREADS = 32 * (GG_EPI_WARP0 + GG_EPI_WARPS);
 constexpr int GG_OUT = 32 * 128;
 constexpr int GG_MAX_PAIRS = 128;
 // Registers per thread: at launch, and of the two kinds of warpgroup after
-// setmaxnreg.  The epilogue holds 128 sums per thread.
+// setmaxnreg.  The epilogue holds 128 sums per thread.  (Spilled, in bytes stored per
+// thread: GM_RDX 12, GM_RDW 66, GM_RDW_CODES 54, GM_WGRAD_CODES 26, the others none.)
 constexpr int GG_REGS = 128, GG_REGS_LOAD = 64, GG_REGS_EPI = 192;
 static_assert(2 * GG_REGS_LOAD + 2 * GG_REGS_EPI <= 4 * GG_REGS, "registers of the block");
 

@@ -314,6 +314,11 @@ int moe_fp8_linear(const void *x_bf16, int T, int N, int K, const void *packed, 
  * Training the router and the projections around the experts.  The pages name
  * no training; these calls use the usual definitions and this library's own
  * routing (moe_route), sort (moe_sort) and FP8 block format (moe_fp8_linear).
+ * moe_forward gives out neither the slots' expert outputs nor the experts' gate
+ * and up activations: dgates (the dot product of dy with a slot's expert output)
+ * and a checkpoint of gate|up come from the caller's own forward pass, as with
+ * dense FP8 projections; from moe_layer_forward alone the router trains by the
+ * balance loss.
  * All are asynchronous and graph-capturable, and their results do not depend
  * on the order in which thread blocks run.  They take at most 2^30 rows.  No
  * output and no workspace (nor moe_route_backward's flag) may overlap an input,
@@ -355,7 +360,8 @@ int moe_balance_loss(const float *logits, const int32_t *topk_idx, const int32_t
  *                 + sum_{j: topk_idx[t, j] = e} gates[t, j] (dgates[t, j] - sum_j' gates[t, j'] dgates[t, j'])
  * with p_t = softmax(logits[t]), f_se = E counts[s, e] / (k n_s), and counts,
  * tokens, seq_offsets, token_mask, S and coef as moe_balance_loss took and gave
- * them (the counts are constants of the gradient).  dloss [1] fp32 device
+ * them (the counts are constants of the gradient).  A row of V_s whose softmax is
+ * NaN gives NaN whatever dloss and coef.  dloss [1] fp32 device
  * pointer, or NULL for no balance term (counts, tokens are not read);
  * dgates [T, k] fp32, or NULL for no gates' term (gates is not read); not both
  * NULL.  The gates' term covers every row, masked or not.  An expert chosen
@@ -378,9 +384,12 @@ int moe_route_backward(const float *logits, const int32_t *topk_idx, const float
  * accumulate 1 adds dw and dbias to what is there (dx is always overwritten;
  * sums below 2^-126 may become 0).
  * The products of fp32 operands are formed from bf16 parts on the tensor cores,
- * accumulated in fp32: dw from all three parts of dlogits (exact), dx from the leading two
- * parts of each operand (about 16 bits, before its rounding to 8).  An infinity
- * in dlogits, x or w_router makes the sums it enters infinite or NaN (in parts,
+ * accumulated in fp32: dw from all three parts of dlogits (exact; a value below
+ * 2^-100 may lose what lies under 2^-126), dx from the leading two
+ * parts of each operand: before its rounding to bf16 dx is off by at most 3 * 2^-16
+ * of its terms' magnitudes and by the accumulation (measured: 0.4 percent of the
+ * entries round to the exact sum's other neighbour).  An infinity in dlogits, x
+ * or w_router makes the sums it enters infinite or NaN (in parts,
  * infinity times a part of 0 is NaN).
  * ws: moe_router_backward_workspace_bytes(T_max, H, E) bytes, 256-byte
  * aligned, T <= T_max; first int32: the error word, cleared by this call
@@ -401,7 +410,7 @@ int moe_router_logits_backward(const float *dlogits, const void *x_bf16, const u
  * max|x| <= 448 * 2^e, byte e + 127, codes rounded to nearest even.  The
  * maximum is taken over finite values; a NaN or infinity is kept as the NaN
  * code 0x7F and restored as NaN; magnitudes above 240 * 2^120 (with e = 120)
- * are kept as that value.  K % 128 == 0; codes and scales contiguous, codes
+ * are kept as that value.  K % 128 == 0, K <= 2^24; codes and scales contiguous, codes
  * 16-byte aligned.  In a call that reads a checkpoint a scale byte 0xFF makes
  * its block NaN. */
 int moe_ckpt_pack(const void *x_bf16, int64_t ldx, int T, int K, uint8_t *codes, uint8_t *scales,
@@ -416,7 +425,8 @@ int moe_ckpt_unpack(const uint8_t *codes, const uint8_t *scales, int T, int K, v
  *   dgu [T, 2I] bf16: dg = dh u s (1 + g (1 - s)), du = dh g s
  *   h   [T, I] bf16 (or NULL): g s u, the activation again for the weight
  *       gradient of the projection behind it
- * fp32, one rounding per output.  I % 128 == 0; all but scales 16-byte aligned. */
+ * fp32 throughout, one rounding per output.  I % 128 == 0, I <= 2^24;
+ * all but scales 16-byte aligned. */
 int moe_ckpt_swiglu_backward(const uint8_t *gu_codes, const uint8_t *gu_scales, const void *dh_bf16,
                              int64_t lddh, int T, int I, void *dgu_bf16, void *h_bf16, cudaStream_t stream);
 
@@ -473,8 +483,8 @@ int moe_ckpt_wgrad(const void *dy_bf16, int64_t lddy, const uint8_t *x_codes, co
  *   shared memory.  One CTA per SM (it takes precedence over
  *   MOE_OPT_TC_PAIR).  Same results.
  *   MOE_OPT_WAIT_LIMIT_US: limit, in microseconds, of every bounded wait inside
- *   the tensor-core GEMM (a pipeline stage normally lands in a few
- *   microseconds).  A wait that runs out raises MOE_FLAG_TIMEOUT in the call's
+ *   the tensor-core GEMMs, the gradients' among them (a pipeline stage normally
+ *   lands in a few microseconds; a call may take longer than the limit).  A wait that runs out raises MOE_FLAG_TIMEOUT in the call's
  *   error word; the kernel still waits (again bounded) for its own copies and
  *   MMAs, frees its tensor memory and returns, and the call's results are
  *   invalid.  Default 1000000 (one second); range [1, 10^7].
@@ -483,7 +493,8 @@ int moe_ckpt_wgrad(const void *dy_bf16, int64_t lddy, const uint8_t *x_codes, co
  *   (neither copied nor signalled), so the MMA waiting for it runs out of
  *   time.  The arming is consumed by that call; 0 disarms.  For tests only.
  *   MOE_OPT_TEST_GRAD_TIMEOUT: the same test of the gradient GEMM's waits: the
- *   next moe_ckpt_wgrad call (R > 0) has each SM pair's first stage withheld.  The arming is consumed by that call; 0 disarms.  For tests only.
+ *   next moe_ckpt_wgrad call (R > 0) has each SM pair's first stage withheld.
+ *   The arming is consumed by that call; 0 disarms.  For tests only.
  * moe_set_option returns MOE_OK or MOE_ERR_INVALID_ARG; moe_get_option returns
  * the current value (-1 for an unknown option). */
 #define MOE_OPT_TC_MIN_ROWS 1
