@@ -996,8 +996,10 @@ __global__ void __launch_bounds__(GG_THREADS, 1)
     // (Its limit counts from the end of this CTA's own work: a wait from the start
     // would bound the whole kernel instead of one hand-over.)
     if (rank != 0 && threadIdx.x == 0) final_wait(smem_u32(&sh.drain), 0);
+    __syncwarp();           // (what follows is of whole warps)
     gg_cluster_sync();      // no remote arrive or MMA targets this CTA any more
     if (threadIdx.x == 0 && *abort) raise_flag(a.flag, FLAG_TIMEOUT);
+    __syncwarp();
     tc_fence_after();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
