@@ -86,10 +86,10 @@ static_assert(2 * GG_REGS_LOAD + 2 * GG_REGS_EPI <= 4 * GG_REGS, "registers of t
 // 512 27.2 / 26.3; 16 groups of 100 rows 222 / 219, of 400 326 / 268, of 800 486 / 467.
 constexpr int kFewRows = 256;
 // Up to this many rows a group, without perm, the kernel reads the codes itself
-// (us, GM_WGRAD_CODES / in front; one group: 512 x 512, 40 rows 8.5 / 8.0; 4096 x 4096, 1
-// row 19.9 / 18.5, 40 rows 20.0 / 19.5, 128 21.6 / 20.6; 16384 x 4096, 64 rows 52 / 57, 128
-// 58 / 60; 16 groups: 2048 x 2048, 40 rows 54 / 59, 4096 x 4096, 16 rows 179 / 201, 64 205 /
-// 216, 128 231 / 216; 128 groups of 1024 x 1024, 128 rows 120 / 135).
+// (us, GM_WGRAD_CODES / in front; one group: 512 x 512, 40 rows 7.4 / 8.0; 4096 x 4096, 1
+// row 19.1 / 18.6, 40 rows 19.1 / 19.5, 128 20.5 / 20.6; 16384 x 4096, 64 rows 52 / 57, 128
+// 58 / 60; 16 groups: 2048 x 2048, 40 rows 54 / 59, 4096 x 4096, 16 rows 179 / 200, 64 203 /
+// 216, 128 230 / 217; 128 groups of 1024 x 1024, 128 rows 118 / 135).
 constexpr int kConvertRows = 128;
 static_assert(kConvertRows <= kFewRows, "the form that converts");
 
@@ -1160,6 +1160,17 @@ __global__ void __launch_bounds__(kSplitThreads) k_grad_prepare(PrepareArgs a) {
     }
 }
 
+// The same for a product that needs nothing else prepared: one warp.  It lets the
+// product's blocks come up in front of its own wait (4096 x 4096, 40 rows: 20.0 us with
+// the usual order, 19.1): they wait for this grid, which has waited for all before
+// it, and by then every block they wait for runs.
+__global__ void __launch_bounds__(32) k_grad_clear(const int32_t* offsets, int G, int R, int32_t* flag) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool bad = __any_sync(0xffffffffu, offsets && bad_offsets(offsets, G, R, threadIdx.x, 32));
+    if (threadIdx.x == 0) *flag = bad ? FLAG_BOUNDS : 0;
+}
+
 static unsigned prepare_ctas(long long items) {
     return (unsigned)std::min<long long>((items + 4 * kSplitThreads - 1) / (4 * kSplitThreads), 148 * 32);
 }
@@ -1335,23 +1346,26 @@ cudaError_t launch_ckpt_wgrad(const void* dy, long long lddy, const uint8_t* cod
     cudaError_t e = cudaSuccess;
     __nv_bfloat16* xb = (__nv_bfloat16*)((char*)ws + 256);
     const bool convert = R > 0 && !perm && R / G <= kConvertRows;
-    // (the form that converts has one CTA here, for the error word and the offsets: a
-    // clear inside the product's grid would not be ordered before another CTA's flag.
-    // It costs 2 us: 512 x 512 6.9 -> 8.5, 4096 x 4096 17.9 -> 19.9)
-    PrepareArgs s = {};
-    s.codes = codes;
-    s.scales = scales;
-    s.items = convert ? 0 : (long long)R * (K / 8);
-    s.K = K;
-    s.perm = perm;
-    s.k_div = k;
-    s.xrows = rows;
-    s.xb = xb;
-    s.offsets = offsets;
-    s.G = G;
-    s.R = R;
-    s.flag = flag;
-    e = launch_pdl(k_grad_prepare, dim3(std::max(1u, prepare_ctas(s.items))), dim3(kSplitThreads), 0, st, s);
+    if (convert) {
+        // (a clear inside the product's grid would not be ordered before another CTA's
+        // flag; this launch costs 1 us: 40 rows, 512 x 512 6.9 -> 7.4, 4096 x 4096 17.9 -> 19.1)
+        e = launch_pdl(k_grad_clear, dim3(1), dim3(32), 0, st, offsets, G, R, flag);
+    } else {
+        PrepareArgs s = {};
+        s.codes = codes;
+        s.scales = scales;
+        s.items = (long long)R * (K / 8);
+        s.K = K;
+        s.perm = perm;
+        s.k_div = k;
+        s.xrows = rows;
+        s.xb = xb;
+        s.offsets = offsets;
+        s.G = G;
+        s.R = R;
+        s.flag = flag;
+        e = launch_pdl(k_grad_prepare, dim3(std::max(1u, prepare_ctas(s.items))), dim3(kSplitThreads), 0, st, s);
+    }
     count_launches(1);
     if (e == cudaSuccess && R == 0) return accumulate ? e : cudaMemsetAsync(dw, 0, sizeof(float) * G * N * K, st);
     CUtensorMap a_map, b_map;

@@ -104,8 +104,9 @@ __device__ __forceinline__ bool packed_header_ok(const void* packed, int H, int 
 // First statement of every kernel launched with launch_pdl: wait until the
 // preceding kernel in the stream has completed and its writes are visible,
 // then allow the next kernel to be scheduled (it waits in turn, so at most two
-// grids overlap and the later one only waits).  Both are no-ops for a launch
-// without the attribute.
+// grids overlap and the later one only waits; a one-warp launch in grad_gemm.cu
+// has the two in the other order).  Both are no-ops for a launch without the
+// attribute.
 __device__ __forceinline__ void pdl_begin() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
